@@ -508,6 +508,118 @@ MOE_API moe_status moe_ep_buffer_open(const uint8_t *ipc_handle, void **ptr);
 MOE_API moe_status moe_ep_buffer_close(void *ptr, int opened);
 
 /*
+ * The gated feed-forward block over expert segments, forward and backward: the
+ * SwiGLU experts of the layer equation on rows that are already grouped by
+ * expert (moe_dispatch's order), or one dense block (n = 1: a shared expert).
+ * Row r belongs to expert e when offsets[e] <= r < offsets[e+1]:
+ *   a = x . w1_e   b = x . w3_e   s = 1 / (1 + e^-a)   h = a s b   y = h . w2_e
+ *   dh = dy . w2_e^T   db = dh a s   da = dh b s (1 + a (1 - s))
+ *   dx = da . w1_e^T + db . w3_e^T
+ *   dw1_e = x^T . da   dw3_e = x^T . db   dw2_e = h^T . dy   (sums over e's rows)
+ * Shapes (the handle's n, d, ffn and dtype; its K is not used):
+ *   x, y, dy, dx [R][d]; gate (a), up (b) [R][ffn]; w1, w3, dw1, dw3
+ *   [n][d][ffn]; w2, dw2 [n][ffn][d]; offsets [n+1] int32 on the device,
+ *   4-byte aligned, or NULL when n = 1 (all R rows).
+ * Products accumulate in fp32.  Rounded to the handle's dtype: every output,
+ * and between the products h (both passes), da and db, once each.  With
+ * the same inputs the results are the same bit for bit.
+ * Offsets must ascend within [0, R]; otherwise every segment is taken as empty
+ * (no row is read or written, weight gradients are zero) and moe_sync_status
+ * reports MOE_ERR_INVALID_ARG.  Rows before offsets[0] and from offsets[n] on
+ * are not touched in y, gate, up and dx.  An expert without rows gets zero
+ * weight gradients.  A NaN or infinity in one expert's rows stays with that
+ * expert.  Outputs must not overlap inputs or one another.
+ * The calls use a workspace of their own in the handle: R * ffn elements
+ * forward, three times that backward.  It grows on demand (not while `stream`
+ * is captured: MOE_ERR_INVALID_ARG then, so call moe_reserve_ffn first) and a
+ * buffer that was replaced lives until moe_destroy, so captured graphs stay
+ * valid.  Calls on one handle share it: order them, graph replays included.
+ *
+ * moe_reserve_ffn: room for R_max rows, for the forward pass (backward = 0) or
+ * both (backward = 1); moe_matmul_mxfp4 needs it only before a capture (R_max
+ * = 1 serves).
+ *   Errors: MOE_ERR_INVALID_ARG (null handle, R_max outside [0, 2^31 - 257],
+ *   backward not 0 or 1, another device), MOE_ERR_UNSUPPORTED, MOE_ERR_ALLOC.
+ */
+MOE_API moe_status moe_reserve_ffn(moe_handle *h, int64_t R_max, int backward);
+
+/*
+ * moe_ffn_forward: y, and with gate and up not NULL the two projections that
+ * the backward pass takes.  R = 0 does nothing.
+ *   Errors: MOE_ERR_INVALID_ARG (R outside [0, 2^31 - 257], null or misaligned
+ *   pointer, one of gate and up null, offsets NULL with n > 1, another device,
+ *   workspace too small under capture), MOE_ERR_UNSUPPORTED, MOE_ERR_ALLOC,
+ *   MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_ffn_forward(moe_handle *h, int64_t R, const int32_t *offsets, const void *x,
+                                   const void *w1, const void *w3, const void *w2, void *gate, void *up,
+                                   void *y, moe_stream_t stream);
+
+/*
+ * moe_ffn_backward: the gradients of sum(dy * y) at the kept projections gate
+ * and up, taken as they are given.  dx may be NULL (not wanted); dw1, dw3 and
+ * dw2 are all given or all NULL; not everything may be NULL.  Gradients are
+ * written, not added to what is there.  R = 0 zeroes the weight gradients.
+ *   Errors: as moe_ffn_forward.
+ */
+MOE_API moe_status moe_ffn_backward(moe_handle *h, int64_t R, const int32_t *offsets, const void *x,
+                                    const void *w1, const void *w3, const void *w2, const void *gate,
+                                    const void *up, const void *dy, void *dx, void *dw1, void *dw3, void *dw2,
+                                    moe_stream_t stream);
+
+/*
+ * Microscaled 4-bit floating point (MXFP4, OCP Microscaling Formats): E2M1
+ * values with one power-of-two scale (E8M0) per 32 consecutive elements.  For
+ * a block v of 32 with m = max|v|:
+ *   scale   = clamp(floor(log2 m) - 2 + 127, 0, 254), 0 when m = 0; it stands
+ *             for 2^(scale - 127)
+ *   code    = E2M1(v / 2^(scale - 127)), to nearest, ties to even, magnitudes
+ *             above 6 to 6; the sign is kept on zeros
+ *   a block with a NaN or an infinity: scale = 255 (NaN), codes 0
+ * codes [..][K/2]: element 2j in the low nibble of byte j, 2j+1 in the high
+ * one; scales [..][K/32].  values (NULL: not wanted) receives what the codes
+ * stand for, in the dtype of the source (exact in both types).
+ *
+ * moe_quantize_mxfp4: x [rows][cols], blocks along the columns; codes
+ * [rows][cols/2], scales [rows][cols/32], values [rows][cols].  rows = 0 does
+ * nothing.
+ * moe_quantize_weights_mxfp4: w [n][rows][cols] as the layer holds its
+ * matrices, blocks along the rows (the reduction); the outputs are turned
+ * over: codes [n][cols][rows/2], scales [n][cols][rows/32], values
+ * [n][cols][rows].
+ * Need no handle; enqueued on `stream`; scales need no alignment.
+ *   Errors: MOE_ERR_INVALID_ARG (rows of moe_quantize_mxfp4 outside [0, 2^31 -
+ *   257], the blocked dimension not a positive multiple of 32, n outside [1,
+ *   65535], cols of the weights outside [1, 2^20], dtype, null / misaligned
+ *   pointer), MOE_ERR_UNSUPPORTED (not an sm_100 device), MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_quantize_mxfp4(int64_t rows, int cols, const void *x, moe_dtype dtype, uint8_t *codes,
+                                      uint8_t *scales, void *values, moe_stream_t stream);
+MOE_API moe_status moe_quantize_weights_mxfp4(int n, int rows, int cols, const void *w, moe_dtype dtype,
+                                              uint8_t *codes, uint8_t *scales, void *values,
+                                              moe_stream_t stream);
+
+/*
+ * Grouped MXFP4 product over the handle's n experts: rows r of expert e
+ * (offsets as above, NULL when n = 1)
+ *   out[r] = A[r] . W_e^T, or with a second matrix
+ *   out[r] = silu(A[r] . W_e^T) (*) (A[r] . P_e^T)   (the gated projections)
+ * A [R][K] and W, P [n][N][K] in MXFP4 (codes [..][K/2], scales [..][K/32]);
+ * out [R][N] in the handle's dtype, rounded once from fp32 accumulators.  N and
+ * K are free (the handle's d, ffn and K are not used).  Rows outside the
+ * segments are not touched; bad offsets as for moe_ffn_forward.  Row and
+ * matrix scales of 255 give NaN.
+ *   Errors: MOE_ERR_INVALID_ARG (R as above, N outside [1, 2^20], K not a
+ *   multiple of 32 in [32, 2^20], null / misaligned pointer, one of the pair's
+ *   null, offsets NULL with n > 1, another device), MOE_ERR_UNSUPPORTED,
+ *   MOE_ERR_ALLOC, MOE_ERR_CUDA.
+ */
+MOE_API moe_status moe_matmul_mxfp4(moe_handle *h, int64_t R, int N, int K, const int32_t *offsets,
+                                    const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *w_codes,
+                                    const uint8_t *w_scales, const uint8_t *pair_codes,
+                                    const uint8_t *pair_scales, void *out, moe_stream_t stream);
+
+/*
  * Debug view of the workspace written by the last forward call: name is "H"
  * (expert hidden layer, [rows][ffn], handle dtype) or "O" (per-row expert
  * outputs, [rows][d], handle dtype for bf16 handles, fp32 for fp32 handles);

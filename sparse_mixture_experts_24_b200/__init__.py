@@ -77,6 +77,12 @@ lib.moe_ep_combine.argtypes = [_vp, _int, _i64, _vp, _vp, _vp, _vp, _vp, _vp]
 lib.moe_ep_buffer_alloc.argtypes = [_i64, ctypes.POINTER(_vp), _vp]
 lib.moe_ep_buffer_open.argtypes = [_vp, ctypes.POINTER(_vp)]
 lib.moe_ep_buffer_close.argtypes = [_vp, _int]
+lib.moe_reserve_ffn.argtypes = [_vp, _i64, _int]
+lib.moe_ffn_forward.argtypes = [_vp, _i64] + [_vp] * 9
+lib.moe_ffn_backward.argtypes = [_vp, _i64] + [_vp] * 13
+lib.moe_quantize_mxfp4.argtypes = [_i64, _int, _vp, _int, _vp, _vp, _vp, _vp]
+lib.moe_quantize_weights_mxfp4.argtypes = [_int, _int, _int, _vp, _int, _vp, _vp, _vp, _vp]
+lib.moe_matmul_mxfp4.argtypes = [_vp, _i64, _int, _int] + [_vp] * 9
 lib.moe_last_error.restype = ctypes.c_char_p
 lib.moe_version.restype = ctypes.c_char_p
 for _f in ("moe_create", "moe_reserve", "moe_forward", "moe_route", "moe_dispatch",
@@ -86,7 +92,8 @@ for _f in ("moe_create", "moe_reserve", "moe_forward", "moe_route", "moe_dispatc
            "moe_forward_expert_choice", "moe_quantize_weights_e4m3", "moe_forward_e4m3",
            "moe_quantize_weights_fp4", "moe_forward_fp4", "moe_pack_weights_w4a4", "moe_forward_w4a4",
            "moe_pack_weights_w4a16", "moe_forward_w4a16", "moe_ep_dispatch", "moe_ep_experts", "moe_ep_combine", "moe_ep_buffer_alloc", "moe_ep_buffer_open",
-           "moe_ep_buffer_close", "moe_set_gate_rounding"):
+           "moe_ep_buffer_close", "moe_set_gate_rounding", "moe_reserve_ffn", "moe_ffn_forward",
+           "moe_ffn_backward", "moe_quantize_mxfp4", "moe_quantize_weights_mxfp4", "moe_matmul_mxfp4"):
     getattr(lib, _f).restype = _int
 
 EXPORTED = ("moe_create", "moe_reserve", "moe_forward", "moe_route", "moe_dispatch",
@@ -97,7 +104,9 @@ EXPORTED = ("moe_create", "moe_reserve", "moe_forward", "moe_route", "moe_dispat
             "moe_quantize_weights_e4m3", "moe_forward_e4m3", "moe_quantize_weights_fp4", "moe_forward_fp4",
             "moe_pack_weights_w4a4", "moe_forward_w4a4", "moe_pack_weights_w4a16", "moe_forward_w4a16",
             "moe_ep_dispatch", "moe_ep_experts", "moe_ep_combine",
-            "moe_ep_buffer_alloc", "moe_ep_buffer_open", "moe_ep_buffer_close", "moe_set_gate_rounding")
+            "moe_ep_buffer_alloc", "moe_ep_buffer_open", "moe_ep_buffer_close", "moe_set_gate_rounding",
+            "moe_reserve_ffn", "moe_ffn_forward", "moe_ffn_backward", "moe_quantize_mxfp4",
+            "moe_quantize_weights_mxfp4", "moe_matmul_mxfp4")
 
 TRACE_STAGES = ("router", "dispatch", "gather", "gemm1", "gemm2", "combine")
 
@@ -382,6 +391,115 @@ def moe_ep_buffer_close(ptr: int, opened: bool) -> None:
     _check(lib.moe_ep_buffer_close(ptr, 1 if opened else 0), "moe_ep_buffer_close")
 
 
+def moe_reserve_ffn(h, R_max: int, backward: int) -> None:
+    _check(lib.moe_reserve_ffn(h, R_max, backward), "moe_reserve_ffn")
+
+
+def moe_ffn_forward(h, R, offsets, x, w1, w3, w2, gate, up, y, stream=None) -> None:
+    _check(lib.moe_ffn_forward(h, R, _ptr(offsets), _ptr(x), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(gate), _ptr(up),
+                               _ptr(y), _stream(stream)), "moe_ffn_forward")
+
+
+def moe_ffn_backward(h, R, offsets, x, w1, w3, w2, gate, up, dy, dx, dw1, dw3, dw2, stream=None) -> None:
+    _check(lib.moe_ffn_backward(h, R, _ptr(offsets), _ptr(x), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(gate), _ptr(up),
+                                _ptr(dy), _ptr(dx), _ptr(dw1), _ptr(dw3), _ptr(dw2), _stream(stream)),
+           "moe_ffn_backward")
+
+
+def moe_quantize_mxfp4(rows, cols, x, dtype, codes, scales, values=None, stream=None) -> None:
+    _check(lib.moe_quantize_mxfp4(rows, cols, _ptr(x), dtype, _ptr(codes), _ptr(scales), _ptr(values),
+                                  _stream(stream)), "moe_quantize_mxfp4")
+
+
+def moe_quantize_weights_mxfp4(n, rows, cols, w, dtype, codes, scales, values=None, stream=None) -> None:
+    _check(lib.moe_quantize_weights_mxfp4(n, rows, cols, _ptr(w), dtype, _ptr(codes), _ptr(scales), _ptr(values),
+                                          _stream(stream)), "moe_quantize_weights_mxfp4")
+
+
+def moe_matmul_mxfp4(h, R, N, K, offsets, a_codes, a_scales, w_codes, w_scales, pair_codes, pair_scales, out,
+                     stream=None) -> None:
+    _check(lib.moe_matmul_mxfp4(h, R, N, K, _ptr(offsets), _ptr(a_codes), _ptr(a_scales), _ptr(w_codes),
+                                _ptr(w_scales), _ptr(pair_codes), _ptr(pair_scales), _ptr(out), _stream(stream)),
+           "moe_matmul_mxfp4")
+
+
+def _refuse(where: str, message: str):
+    raise MoEError(MOE_ERR_INVALID_ARG, where, message)
+
+
+def _take(where: str, name: str, t, dtype, shape):
+    """Refuse a tensor that the C ABI would misread: `t` has to be a contiguous
+    CUDA tensor of this type and shape on the current device."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _refuse(where, "%s is not a CUDA tensor" % name)
+    if t.dtype != dtype:
+        _refuse(where, "%s is %s, not %s" % (name, t.dtype, dtype))
+    if tuple(t.shape) != tuple(shape):
+        _refuse(where, "%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        _refuse(where, "%s is not contiguous" % name)
+    if t.device.index != torch.cuda.current_device():
+        _refuse(where, "%s is on %s, the current device is %d" % (name, t.device, torch.cuda.current_device()))
+
+
+def _on(stream):
+    """Context in which outputs are allocated: the stream the kernels run on,
+    so that the allocator does not hand out memory still in use there."""
+    import torch
+    if stream is None:
+        return torch.cuda.stream(torch.cuda.current_stream())
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def _mx_dtype(where: str, name: str, t):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _refuse(where, "%s is not a CUDA tensor" % name)
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        _refuse(where, "%s is %s, not bfloat16 or float32" % (name, t.dtype))
+    return MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32
+
+
+def quantize_mxfp4(x, values: bool = False, stream=None):
+    """x [..., cols] (torch bf16 or fp32, CUDA, contiguous), blocks of 32 along
+    cols -> (codes uint8 [..., cols/2], scales uint8 [..., cols/32]), and with
+    values=True also the tensor that they stand for, in x's type."""
+    import torch
+    where = "quantize_mxfp4"
+    dt = _mx_dtype(where, "x", x)
+    if x.dim() < 1 or x.shape[-1] < 32 or x.shape[-1] % 32:
+        _refuse(where, "x has shape %s: the last dimension must be a positive multiple of 32" % (tuple(x.shape),))
+    _take(where, "x", x, x.dtype, x.shape)
+    cols = x.shape[-1]
+    with _on(stream):
+        codes = torch.empty(*x.shape[:-1], cols // 2, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(*x.shape[:-1], cols // 32, dtype=torch.uint8, device=x.device)
+        v = torch.empty_like(x) if values else None
+    moe_quantize_mxfp4(x.numel() // cols, cols, x, dt, codes, scales, v, stream)
+    return (codes, scales, v) if values else (codes, scales)
+
+
+def quantize_weights_mxfp4(w, values: bool = False, stream=None):
+    """w [n][rows][cols] (torch bf16 or fp32, CUDA, contiguous), blocks of 32
+    along rows -> (codes uint8 [n][cols][rows/2], scales uint8 [n][cols][rows/32]),
+    and with values=True also what they stand for, [n][cols][rows] in w's type."""
+    import torch
+    where = "quantize_weights_mxfp4"
+    dt = _mx_dtype(where, "w", w)
+    if w.dim() != 3 or w.shape[1] < 32 or w.shape[1] % 32:
+        _refuse(where, "w has shape %s: [n][rows][cols] with rows a positive multiple of 32 is wanted"
+                % (tuple(w.shape),))
+    _take(where, "w", w, w.dtype, w.shape)
+    n, rows, cols = w.shape
+    with _on(stream):
+        codes = torch.empty(n, cols, rows // 2, dtype=torch.uint8, device=w.device)
+        scales = torch.empty(n, cols, rows // 32, dtype=torch.uint8, device=w.device)
+        v = torch.empty(n, cols, rows, dtype=w.dtype, device=w.device) if values else None
+    moe_quantize_weights_mxfp4(n, rows, cols, w, dt, codes, scales, v, stream)
+    return (codes, scales, v) if values else (codes, scales)
+
+
 def moe_set_gate_rounding(h, bf16: int) -> None:
     _check(lib.moe_set_gate_rounding(h, bf16), "moe_set_gate_rounding")
 
@@ -510,6 +628,95 @@ class MoELayer:
             topk_w = torch.empty((T, self.K), dtype=torch.float32, device=x.device)
         moe_forward_w4a16(self.h, T, x, W_g, *w13, *w2, y, topk_idx, topk_w, stream)
         return y, topk_idx, topk_w
+
+    def _torch_dtype(self):
+        import torch
+        return torch.bfloat16 if self.dtype == "bf16" else torch.float32
+
+    def _ffn_check(self, where, x, w1, w3, w2, offsets):
+        import torch
+        dt, n, d, F = self._torch_dtype(), self.n, self.d, self.ffn
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            _refuse(where, "x is not a [rows][%d] tensor" % d)
+        _take(where, "x", x, dt, (x.shape[0], d))
+        _take(where, "w1", w1, dt, (n, d, F))
+        _take(where, "w3", w3, dt, (n, d, F))
+        _take(where, "w2", w2, dt, (n, F, d))
+        if offsets is not None:
+            _take(where, "offsets", offsets, torch.int32, (n + 1,))
+        return x.shape[0]
+
+    def reserve_ffn(self, R_max: int, backward: bool = True) -> None:
+        """Workspace of ffn_forward (and ffn_backward) for up to R_max rows."""
+        moe_reserve_ffn(self.h, R_max, 1 if backward else 0)
+
+    def ffn_forward(self, x, w1, w3, w2, offsets=None, keep: bool = False, y=None, stream=None):
+        """The experts' gated feed-forward block on rows grouped by expert:
+        rows offsets[e] .. offsets[e+1]-1 of x [R][d] belong to expert e
+        (offsets int32 [n+1]; None with n = 1: all rows).  -> y [R][d], or with
+        keep=True (y, gate, up): the projections [R][ffn] for ffn_backward.
+        Rows outside the segments are left as they were in y (uninitialised
+        when y is allocated here)."""
+        import torch
+        where = "ffn_forward"
+        R = self._ffn_check(where, x, w1, w3, w2, offsets)
+        with _on(stream):
+            if y is None:
+                y = torch.empty_like(x)
+            gate = torch.empty(R, self.ffn, dtype=x.dtype, device=x.device) if keep else None
+            up = torch.empty_like(gate) if keep else None
+        _take(where, "y", y, x.dtype, x.shape)
+        moe_ffn_forward(self.h, R, offsets, x, w1, w3, w2, gate, up, y, stream)
+        return (y, gate, up) if keep else y
+
+    def ffn_backward(self, dy, x, gate, up, w1, w3, w2, offsets=None, need_dx: bool = True, need_dw: bool = True,
+                     stream=None):
+        """Gradients of the block for dy [R][d], at the gate and up that
+        ffn_forward(keep=True) returned -> (dx, dw1, dw3, dw2); dx is None with
+        need_dx=False, the weight gradients with need_dw=False."""
+        import torch
+        where = "ffn_backward"
+        R = self._ffn_check(where, x, w1, w3, w2, offsets)
+        _take(where, "dy", dy, x.dtype, x.shape)
+        _take(where, "gate", gate, x.dtype, (R, self.ffn))
+        _take(where, "up", up, x.dtype, (R, self.ffn))
+        with _on(stream):
+            dx = torch.empty_like(x) if need_dx else None
+            dw = [torch.empty_like(w) if need_dw else None for w in (w1, w3, w2)]
+        moe_ffn_backward(self.h, R, offsets, x, w1, w3, w2, gate, up, dy, dx, *dw, stream)
+        return (dx, *dw)
+
+    def matmul_mxfp4(self, a, w, pair=None, offsets=None, out=None, stream=None):
+        """Grouped product of MXFP4 rows with the MXFP4 matrices of their expert
+        -> out [R][N] in the layer's dtype.  a = (codes [R][K/2], scales
+        [R][K/32]) from quantize_mxfp4; w = (codes [n][N][K/2], scales
+        [n][N][K/32]) from quantize_weights_mxfp4; pair = the same of a second
+        matrix: out = silu(a . w^T) * (a . pair^T).  N and K are free."""
+        import torch
+        where = "matmul_mxfp4"
+        for name, t, dims in (("a codes", a[0], 2), ("w codes", w[0], 3)):
+            if not isinstance(t, torch.Tensor) or t.dim() != dims:
+                _refuse(where, "%s is not a tensor of %d dimensions" % (name, dims))
+        R, K, N = a[0].shape[0], 2 * a[0].shape[1], w[0].shape[1]
+        if K < 32 or K % 32:
+            _refuse(where, "K = %d is not a positive multiple of 32" % K)
+        u8 = torch.uint8
+        _take(where, "a codes", a[0], u8, (R, K // 2))
+        _take(where, "a scales", a[1], u8, (R, K // 32))
+        for name, m in (("w", w), ("pair", pair)):
+            if m is not None:
+                _take(where, name + " codes", m[0], u8, (self.n, N, K // 2))
+                _take(where, name + " scales", m[1], u8, (self.n, N, K // 32))
+        if offsets is not None:
+            _take(where, "offsets", offsets, torch.int32, (self.n + 1,))
+        dt = self._torch_dtype()
+        if out is None:
+            with _on(stream):
+                out = torch.empty(R, N, dtype=dt, device=a[0].device)
+        _take(where, "out", out, dt, (R, N))
+        p = pair if pair is not None else (None, None)
+        moe_matmul_mxfp4(self.h, R, N, K, offsets, *a[:2], *w[:2], *p[:2], out, stream)
+        return out
 
     def set_capacity_factor(self, factor: float) -> None:
         moe_set_capacity_factor(self.h, factor)

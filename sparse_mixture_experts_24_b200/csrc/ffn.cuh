@@ -1,0 +1,83 @@
+// ffn.cuh -- what the kernels of the gated feed-forward block over expert
+// segments (ffn_simt.cu, gemm_ffn.cu) and of the grouped MXFP4 product share:
+// the segment plan that every block derives from the caller's offsets, and the
+// block's formulas.
+//
+//   a = x . w1_e, b = x . w3_e, s = 1 / (1 + e^-a), h = a s b, y = h . w2_e
+//   dh = dy . w2_e^T, db = dh a s, da = dh b s (1 + a (1 - s))
+//   dx = da . w1_e^T + db . w3_e^T, dw1 = x^T . da, dw3 = x^T . db, dw2 = h^T . dy
+//
+// Source of the forward: SwiGLU_i(x) = (silu(x.w1_i) (*) x.w3_i) . w2_i
+// ("Mixtral of Experts" section 2.1, flash-card page); the backward is its
+// derivative.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kFfnMaxExperts = 256;
+
+// Segment plan in shared memory: expert e holds rows off[e] .. off[e+1]-1, cut
+// into blocks of block_rows rows; blk is the exclusive prefix of the blocks.
+struct SegmentPlan {
+    int32_t off[kFfnMaxExperts + 1];
+    int32_t blk[kFfnMaxExperts + 1];
+};
+
+// Every thread of the block (a multiple of 32, at least 32) calls this.
+// Offsets come from the caller's device memory: unless they ascend within
+// [0, R], every segment is taken as empty and kStatusOffsets is set, so no
+// kernel ever addresses a row outside the caller's buffers.  A null `offsets`
+// means one segment of all R rows (n = 1).
+__device__ __forceinline__ void load_plan(SegmentPlan& p, const int32_t* offsets, int n, int64_t R, int block_rows,
+                                          int* status) {
+    const int tid = threadIdx.x, nt = blockDim.x;
+    for (int i = tid; i <= n; i += nt)
+        p.off[i] = offsets ? __ldg(offsets + i) : (i == 0 ? 0 : static_cast<int32_t>(R));
+    __syncthreads();
+    int bad = 0;
+    for (int i = tid; i <= n; i += nt) {
+        const int32_t v = p.off[i];
+        if (v < 0 || v > R || (i > 0 && v < p.off[i - 1])) bad = 1;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) {
+        for (int i = tid; i <= n; i += nt) p.off[i] = p.blk[i] = 0;
+        if (tid == 0 && status) atomicOr(status, kStatusOffsets);
+        __syncthreads();
+        return;
+    }
+    if (tid < 32) {
+        int base = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + tid;
+            const int own = i < n ? (p.off[i + 1] - p.off[i] + block_rows - 1) / block_rows : 0;
+            int incl = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (tid >= o) incl += u;
+            }
+            if (i < n) p.blk[i] = base + incl - own;
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (tid == 0) p.blk[n] = base;
+    }
+    __syncthreads();
+}
+
+// Expert that owns row block `b` (b < blk[n]).
+__device__ __forceinline__ int plan_expert(const SegmentPlan& p, int n, int b) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.blk[mid] <= b)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+}  // namespace moe

@@ -1,0 +1,328 @@
+// ffn_api.cu -- the C ABI of the gated feed-forward block over expert segments
+// (forward, backward) and of MXFP4 (quantisation, grouped product), declared in
+// include/moe.h: argument checks, workspace, launch sequences.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/moe.h"
+#include "handle.h"
+#include "kernels.h"
+
+using moe_api_detail::done;
+using moe_api_detail::failed;
+using moe_api_detail::HandleView;
+using moe_api_detail::open_handle;
+
+namespace {
+
+moe_status cuda_failed(cudaError_t e, const char* what) {
+    return failed(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+#define FFN_REQUIRE_PTR(p)                                                                      \
+    do {                                                                                        \
+        if (!(p)) return failed(MOE_ERR_INVALID_ARG, "%s is NULL", #p);                         \
+        if (!aligned16(p)) return failed(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p); \
+    } while (0)
+
+moe_status check_rows(int64_t R, const char* name = "R") {
+    if (R < 0) return failed(MOE_ERR_INVALID_ARG, "%s = %lld < 0", name, static_cast<long long>(R));
+    if (R > 2147483647LL - 256)
+        return failed(MOE_ERR_INVALID_ARG, "%s = %lld exceeds 2^31 - 257", name, static_cast<long long>(R));
+    return MOE_OK;
+}
+
+// offsets may be left out for one expert only; 4-byte integers, so their own
+// alignment is what is asked of them.
+moe_status check_offsets(int n, const int32_t* offsets) {
+    if (!offsets && n != 1) return failed(MOE_ERR_INVALID_ARG, "offsets is NULL with n = %d experts", n);
+    if (reinterpret_cast<uintptr_t>(offsets) & 3u)
+        return failed(MOE_ERR_INVALID_ARG, "offsets is not 4-byte aligned");
+    return MOE_OK;
+}
+
+moe_status allocate(moe::FfnWorkspace* w, size_t bytes, cudaStream_t st, bool use_stream, void** out) {
+    if (use_stream) {
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        cudaError_t e = cudaStreamIsCapturing(st, &cap);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return cuda_failed(e, "cudaStreamIsCapturing");
+        }
+        if (cap != cudaStreamCaptureStatusNone)
+            return failed(MOE_ERR_INVALID_ARG,
+                          "the workspace is too small and cannot grow while the stream is captured: call "
+                          "moe_reserve_ffn first");
+    }
+    void* p = nullptr;
+    cudaError_t e = cudaMalloc(&p, bytes);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return failed(MOE_ERR_ALLOC, "cudaMalloc(%zu bytes) for the workspace failed: %s", bytes,
+                      cudaGetErrorString(e));
+    }
+    w->allocations.push_back(p);
+    *out = p;
+    return MOE_OK;
+}
+
+// The status word, allocated once; then room for `rows` hidden rows and, for
+// the backward pass, their gradients.
+moe_status need(const HandleView& v, int64_t rows, bool backward, cudaStream_t st, bool use_stream) {
+    moe::FfnWorkspace* w = v.ffn;
+    if (!w->status) {
+        void* p = nullptr;
+        moe_status s = allocate(w, 256, st, use_stream, &p);
+        if (s != MOE_OK) return s;
+        cudaError_t e = cudaMemset(p, 0, 256);
+        if (e != cudaSuccess) return cuda_failed(e, "cudaMemset(status)");
+        w->status = static_cast<int*>(p);
+    }
+    const size_t row = static_cast<size_t>(v.F) * (v.bf16 ? 2 : 4);
+    if (rows > w->h_rows) {
+        moe_status s = allocate(w, row * rows, st, use_stream, &w->h);
+        if (s != MOE_OK) return s;
+        w->h_rows = rows;
+    }
+    if (backward && rows > w->grad_rows) {
+        void* p = nullptr;
+        moe_status s = allocate(w, 2 * row * rows, st, use_stream, &p);
+        if (s != MOE_OK) return s;
+        w->da = p;
+        w->db = static_cast<uint8_t*>(p) + row * rows;
+        w->grad_rows = rows;
+    }
+    return MOE_OK;
+}
+
+moe::FfnArgs ffn_args(const HandleView& v, int64_t R, const int32_t* offsets) {
+    moe::FfnArgs a{};
+    a.offsets = offsets;
+    a.n = v.n;
+    a.R = R;
+    a.d = v.d;
+    a.F = v.F;
+    a.h = v.ffn->h;
+    a.da = v.ffn->da;
+    a.db = v.ffn->db;
+    a.status = v.ffn->status;
+    return a;
+}
+
+moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t st, const char* what) {
+    cudaError_t e = moe::launch_ffn_simt(op, v.bf16, a, st);
+    if (e != cudaSuccess) return cuda_failed(e, what);
+    *v.launches += 1;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_reserve_ffn(moe_handle* h, int64_t R_max, int backward) {
+    if (!h) return failed(MOE_ERR_INVALID_ARG, "null handle");
+    moe_status s = check_rows(R_max, "R_max");
+    if (s != MOE_OK) return s;
+    if (backward != 0 && backward != 1)
+        return failed(MOE_ERR_INVALID_ARG, "backward = %d is neither 0 nor 1", backward);
+    if (R_max == 0) return done();
+    HandleView v;
+    s = open_handle(h, &v);
+    if (s != MOE_OK) return s;
+    s = need(v, R_max, backward == 1, nullptr, false);
+    return s == MOE_OK ? done() : s;
+}
+
+moe_status moe_ffn_forward(moe_handle* h, int64_t R, const int32_t* offsets, const void* x, const void* w1,
+                           const void* w3, const void* w2, void* gate, void* up, void* y, moe_stream_t stream) {
+    if (!h) return failed(MOE_ERR_INVALID_ARG, "null handle");
+    moe_status s = check_rows(R);
+    if (s != MOE_OK) return s;
+    if (R == 0) return done();
+    FFN_REQUIRE_PTR(x);
+    FFN_REQUIRE_PTR(w1);
+    FFN_REQUIRE_PTR(w3);
+    FFN_REQUIRE_PTR(w2);
+    FFN_REQUIRE_PTR(y);
+    if ((gate == nullptr) != (up == nullptr))
+        return failed(MOE_ERR_INVALID_ARG, "gate and up must both be given or both be null");
+    if (gate) {
+        FFN_REQUIRE_PTR(gate);
+        FFN_REQUIRE_PTR(up);
+    }
+    HandleView v;
+    s = open_handle(h, &v);
+    if (s != MOE_OK) return s;
+    s = check_offsets(v.n, offsets);
+    if (s != MOE_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    s = need(v, R, false, st, true);
+    if (s != MOE_OK) return s;
+    moe::FfnArgs a = ffn_args(v, R, offsets);
+    a.x = x;
+    a.w1 = w1;
+    a.w3 = w3;
+    a.w2 = w2;
+    a.gate = gate;
+    a.up = up;
+    a.y = y;
+    moe::chain_begin();
+    s = run(v, moe::kFfnUp, a, st, "feed-forward projections launch");
+    if (s != MOE_OK) return s;
+    s = run(v, moe::kFfnDown, a, st, "feed-forward output launch");
+    return s == MOE_OK ? done() : s;
+}
+
+moe_status moe_ffn_backward(moe_handle* h, int64_t R, const int32_t* offsets, const void* x, const void* w1,
+                            const void* w3, const void* w2, const void* gate, const void* up, const void* dy,
+                            void* dx, void* dw1, void* dw3, void* dw2, moe_stream_t stream) {
+    if (!h) return failed(MOE_ERR_INVALID_ARG, "null handle");
+    moe_status s = check_rows(R);
+    if (s != MOE_OK) return s;
+    if ((dw1 == nullptr) != (dw3 == nullptr) || (dw1 == nullptr) != (dw2 == nullptr))
+        return failed(MOE_ERR_INVALID_ARG, "dw1, dw3 and dw2 must all be given or all be null");
+    if (!dx && !dw1) return failed(MOE_ERR_INVALID_ARG, "neither dx nor the weight gradients are asked for");
+    if (dw1) {
+        FFN_REQUIRE_PTR(dw1);
+        FFN_REQUIRE_PTR(dw3);
+        FFN_REQUIRE_PTR(dw2);
+    }
+    if (R > 0) {
+        if (dx) FFN_REQUIRE_PTR(dx);
+        FFN_REQUIRE_PTR(x);
+        FFN_REQUIRE_PTR(w1);
+        FFN_REQUIRE_PTR(w3);
+        FFN_REQUIRE_PTR(w2);
+        FFN_REQUIRE_PTR(gate);
+        FFN_REQUIRE_PTR(up);
+        FFN_REQUIRE_PTR(dy);
+    }
+    HandleView v;
+    s = open_handle(h, &v);
+    if (s != MOE_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (R == 0) {  // no rows: the weight gradients are zero
+        const size_t bytes = static_cast<size_t>(v.n) * v.d * v.F * (v.bf16 ? 2 : 4);
+        for (void* p : {dw1, dw3, dw2}) {
+            cudaError_t e = p ? cudaMemsetAsync(p, 0, bytes, st) : cudaSuccess;
+            if (e != cudaSuccess) return cuda_failed(e, "cudaMemsetAsync(weight gradients)");
+        }
+        return done();
+    }
+    s = check_offsets(v.n, offsets);
+    if (s != MOE_OK) return s;
+    s = need(v, R, true, st, true);
+    if (s != MOE_OK) return s;
+    moe::FfnArgs a = ffn_args(v, R, offsets);
+    a.x = x;
+    a.dy = dy;
+    a.w1 = w1;
+    a.w3 = w3;
+    a.w2 = w2;
+    a.gate = const_cast<void*>(gate);
+    a.up = const_cast<void*>(up);
+    a.dx = dx;
+    a.dw1 = dw1;
+    a.dw3 = dw3;
+    a.dw2 = dw2;
+    moe::chain_begin();
+    s = run(v, moe::kFfnGrad, a, st, "feed-forward hidden gradient launch");
+    if (s == MOE_OK && dx) s = run(v, moe::kFfnDx, a, st, "feed-forward input gradient launch");
+    if (s == MOE_OK && dw1) s = run(v, moe::kFfnDw, a, st, "feed-forward weight gradient launch");
+    return s == MOE_OK ? done() : s;
+}
+
+namespace {
+moe_status device_of_call(int* sms) {
+    int dev = 0, major = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_failed(e, "cudaGetDevice");
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (major != 10) return failed(MOE_ERR_UNSUPPORTED, "device %d is not sm_100", dev);
+    return MOE_OK;
+}
+}  // namespace
+
+moe_status moe_quantize_mxfp4(int64_t rows, int cols, const void* x, moe_dtype dtype, uint8_t* codes,
+                              uint8_t* scales, void* values, moe_stream_t stream) {
+    moe_status s = check_rows(rows, "rows");
+    if (s != MOE_OK) return s;
+    if (cols < 32 || cols % 32 != 0)
+        return failed(MOE_ERR_INVALID_ARG, "cols = %d is not a positive multiple of 32", cols);
+    if (dtype != MOE_F32 && dtype != MOE_BF16)
+        return failed(MOE_ERR_INVALID_ARG, "dtype = %d is not MOE_F32 or MOE_BF16", static_cast<int>(dtype));
+    if (rows == 0) return done();
+    FFN_REQUIRE_PTR(x);
+    FFN_REQUIRE_PTR(codes);
+    if (!scales) return failed(MOE_ERR_INVALID_ARG, "scales is NULL");
+    if (values) FFN_REQUIRE_PTR(values);
+    int sms = 0;
+    s = device_of_call(&sms);
+    if (s != MOE_OK) return s;
+    cudaError_t e = moe::launch_mx_rows(x, dtype == MOE_BF16, rows, cols, codes, scales, values, sms,
+                                        reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_failed(e, "MXFP4 quantisation launch");
+    return done();
+}
+
+moe_status moe_quantize_weights_mxfp4(int n, int rows, int cols, const void* w, moe_dtype dtype, uint8_t* codes,
+                                      uint8_t* scales, void* values, moe_stream_t stream) {
+    if (n < 1 || n > 65535) return failed(MOE_ERR_INVALID_ARG, "n = %d outside [1, 65535]", n);
+    if (rows < 32 || rows % 32 != 0)
+        return failed(MOE_ERR_INVALID_ARG, "rows = %d is not a positive multiple of 32", rows);
+    if (cols < 1 || cols > 1048576) return failed(MOE_ERR_INVALID_ARG, "cols = %d outside [1, 1048576]", cols);
+    if (dtype != MOE_F32 && dtype != MOE_BF16)
+        return failed(MOE_ERR_INVALID_ARG, "dtype = %d is not MOE_F32 or MOE_BF16", static_cast<int>(dtype));
+    FFN_REQUIRE_PTR(w);
+    FFN_REQUIRE_PTR(codes);
+    if (!scales) return failed(MOE_ERR_INVALID_ARG, "scales is NULL");
+    if (values) FFN_REQUIRE_PTR(values);
+    int sms = 0;
+    moe_status s = device_of_call(&sms);
+    if (s != MOE_OK) return s;
+    cudaError_t e = moe::launch_mx_weights(w, dtype == MOE_BF16, n, rows, cols, codes, scales, values,
+                                           reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_failed(e, "MXFP4 weight quantisation launch");
+    return done();
+}
+
+moe_status moe_matmul_mxfp4(moe_handle* h, int64_t R, int N, int K, const int32_t* offsets, const uint8_t* a_codes,
+                            const uint8_t* a_scales, const uint8_t* w_codes, const uint8_t* w_scales,
+                            const uint8_t* pair_codes, const uint8_t* pair_scales, void* out, moe_stream_t stream) {
+    if (!h) return failed(MOE_ERR_INVALID_ARG, "null handle");
+    moe_status s = check_rows(R);
+    if (s != MOE_OK) return s;
+    if (N < 1 || N > 1048576) return failed(MOE_ERR_INVALID_ARG, "N = %d outside [1, 1048576]", N);
+    if (K < 32 || K % 32 != 0 || K > 1048576)
+        return failed(MOE_ERR_INVALID_ARG, "K = %d is not a multiple of 32 in [32, 1048576]", K);
+    if ((pair_codes == nullptr) != (pair_scales == nullptr))
+        return failed(MOE_ERR_INVALID_ARG, "pair_codes and pair_scales must both be given or both be null");
+    if (R == 0) return done();
+    FFN_REQUIRE_PTR(a_codes);
+    FFN_REQUIRE_PTR(w_codes);
+    if (pair_codes) FFN_REQUIRE_PTR(pair_codes);
+    FFN_REQUIRE_PTR(out);
+    if (!a_scales) return failed(MOE_ERR_INVALID_ARG, "a_scales is NULL");
+    if (!w_scales) return failed(MOE_ERR_INVALID_ARG, "w_scales is NULL");
+    HandleView v;
+    s = open_handle(h, &v);
+    if (s != MOE_OK) return s;
+    s = check_offsets(v.n, offsets);
+    if (s != MOE_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    s = need(v, 0, false, st, true);
+    if (s != MOE_OK) return s;
+    moe::MxGemmArgs a{offsets,  v.n,      R,          N,           K,   a_codes,      a_scales,
+                      w_codes,  w_scales, pair_codes, pair_scales, out, v.ffn->status};
+    moe::chain_begin();
+    cudaError_t e = moe::launch_mx_gemm(a, v.bf16, v.num_sms, st);
+    if (e != cudaSuccess) return cuda_failed(e, "MXFP4 product launch");
+    *v.launches += 1;
+    return done();
+}
+
+}  // extern "C"

@@ -1,0 +1,296 @@
+// ffn_simt.cu -- the gated feed-forward block over expert segments, forward
+// and backward, on the CUDA cores: fp32 multiply-adds for both types.
+//
+// Five products share one kernel (ffn.cuh has the formulas):
+//   kFfnUp    [a | b] = x . [w1 | w3] -> h (and a, b when they are kept)
+//   kFfnDown  y = h . w2
+//   kFfnGrad  dh = dy . w2^T -> da, db and h from a, b
+//   kFfnDx    dx = da . w1^T + db . w3^T (one sum over both)
+//   kFfnDw    [dw1 | dw3] = x^T . [da | db] and dw2 = h^T . dy, all in one launch
+//
+// A block owns 64 x 128 outputs, 128 threads hold 8 x 8 each: per reduction
+// step a thread reads 16 values from shared memory for 64 multiply-adds.  The
+// 128 columns are two halves of 64 (thread columns 4 tx .. 4 tx + 3 of either),
+// so that the pairs a, b and da, db of one hidden column meet in one thread.
+// The reduction runs in chunks of 16 through two shared-memory buffers, the
+// next chunk's global loads in flight while the current one is multiplied.
+#include <cstddef>
+
+#include "ffn.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace ffn_simt {
+
+constexpr int kM = 64, kN = 128, kK = 16, kThreads = 128;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const void* p, int64_t i);
+template <>
+__device__ __forceinline__ float4 load4<float>(const void* p, int64_t i) {
+    return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+}
+template <>
+__device__ __forceinline__ float4 load4<uint16_t>(const void* p, int64_t i) {
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
+    float4 v;
+    unpack_bf16x2(q.x, v.x, v.y);
+    unpack_bf16x2(q.y, v.z, v.w);
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(void* p, int64_t i, float a, float b, float c, float d);
+template <>
+__device__ __forceinline__ void store4<float>(void* p, int64_t i, float a, float b, float c, float d) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(a, b, c, d);
+}
+template <>
+__device__ __forceinline__ void store4<uint16_t>(void* p, int64_t i, float a, float b, float c, float d) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+}
+
+struct __align__(16) Smem {
+    float a[2][kK][kM + 4];  // rows of both arrays stay 16-byte aligned: they are read as float4
+    float b[2][kK][kN + 4];
+    SegmentPlan plan;
+};
+static_assert((kM + 4) % 4 == 0 && (kN + 4) % 4 == 0 && offsetof(Smem, b) % 16 == 0, "float4 alignment");
+
+}  // namespace ffn_simt
+
+using namespace ffn_simt;
+
+template <typename T, int kOp>
+__global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
+    griddep_wait();
+    __shared__ Smem sm;
+    load_plan(sm.plan, g.offsets, g.n, g.R, kM, g.status);
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int d = g.d, F = g.F;
+
+    // the tile: expert, first output row (row ops: a row of the batch) and the
+    // rows inside it, the column half starts, and the reduction
+    int e, row0, rows, col[2];
+    int64_t K;
+    bool dw2 = false;
+    if (kOp == kFfnDw) {
+        e = blockIdx.y;
+        const int t13 = (d / kM) * (F / 64), t = blockIdx.x;
+        dw2 = t >= t13;
+        const int nc = dw2 ? (d + kN - 1) / kN : F / 64;
+        const int local = dw2 ? t - t13 : t;
+        row0 = (local / nc) * kM;
+        rows = kM;
+        const int c = local % nc;
+        col[0] = dw2 ? c * kN : c * 64;
+        col[1] = dw2 ? c * kN + 64 : c * 64;
+        K = sm.plan.off[e + 1] - sm.plan.off[e];
+    } else {
+        if (static_cast<int>(blockIdx.x) >= sm.plan.blk[g.n]) return;
+        e = plan_expert(sm.plan, g.n, blockIdx.x);
+        row0 = sm.plan.off[e] + (static_cast<int>(blockIdx.x) - sm.plan.blk[e]) * kM;
+        rows = min(kM, sm.plan.off[e + 1] - row0);
+        const int c = blockIdx.y;
+        col[0] = kOp == kFfnUp ? c * 64 : c * kN;
+        col[1] = kOp == kFfnUp ? c * 64 : c * kN + 64;
+        K = kOp == kFfnUp || kOp == kFfnGrad ? d : (kOp == kFfnDown ? F : 2 * F);
+    }
+    const int cols = kOp == kFfnUp || kOp == kFfnGrad ? F : (kOp == kFfnDw && !dw2 ? F : d);
+    const int64_t w_at = static_cast<int64_t>(e) * d * F;
+    const int64_t seg0 = kOp == kFfnDw ? sm.plan.off[e] : 0;
+
+    // this thread's four-element pieces of a chunk: 2 of A (64 x 16), 4 of B (16 x 128)
+    float4 ra[2], rb[4];
+    auto fetch = [&](int64_t k0) {
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int p = tid + i * kThreads;
+            if (kOp == kFfnDw) {  // A(m, k) = row k of x (or h), feature m: 16 pieces of a row
+                const int64_t k = k0 + (p >> 4);
+                const int m = row0 + (p & 15) * 4;
+                ra[i] = k < K ? (dw2 ? load4<T>(g.h, (seg0 + k) * F + m) : load4<T>(g.x, (seg0 + k) * d + m)) : zero;
+            } else {
+                const int r = p >> 2;
+                const int64_t k = k0 + (p & 3) * 4;
+                const int64_t row = static_cast<int64_t>(row0) + r;
+                if (r >= rows)
+                    ra[i] = zero;
+                else if (kOp == kFfnUp)
+                    ra[i] = load4<T>(g.x, row * d + k);
+                else if (kOp == kFfnDown)
+                    ra[i] = load4<T>(g.h, row * F + k);
+                else if (kOp == kFfnGrad)
+                    ra[i] = load4<T>(g.dy, row * d + k);
+                else
+                    ra[i] = k < F ? load4<T>(g.da, row * F + k) : load4<T>(g.db, row * F + k - F);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = tid + i * kThreads;
+            if (kOp == kFfnGrad || kOp == kFfnDx) {  // B(n, k): the weights' rows, k contiguous
+                const int n = p >> 2;
+                const int64_t k = k0 + (p & 3) * 4;
+                const int64_t c = col[n >> 6] + (n & 63);
+                if (c >= cols)
+                    rb[i] = zero;
+                else if (kOp == kFfnGrad)
+                    rb[i] = load4<T>(g.w2, w_at + c * d + k);
+                else
+                    rb[i] = k < F ? load4<T>(g.w1, w_at + c * F + k) : load4<T>(g.w3, w_at + c * F + k - F);
+            } else {  // n contiguous
+                const int64_t k = k0 + (p >> 5);
+                const int n = (p & 31) * 4, half = n >> 6;
+                const int64_t c = col[half] + (n & 63);
+                if (c >= cols || k >= K)
+                    rb[i] = zero;
+                else if (kOp == kFfnUp)
+                    rb[i] = load4<T>(half ? g.w3 : g.w1, w_at + k * F + c);
+                else if (kOp == kFfnDown)
+                    rb[i] = load4<T>(g.w2, w_at + k * d + c);
+                else if (dw2)
+                    rb[i] = load4<T>(g.dy, (seg0 + k) * d + c);
+                else
+                    rb[i] = load4<T>(half ? g.db : g.da, (seg0 + k) * F + c);
+            }
+        }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int p = tid + i * kThreads;
+            if (kOp == kFfnDw) {
+                *reinterpret_cast<float4*>(&sm.a[buf][p >> 4][(p & 15) * 4]) = ra[i];
+            } else {
+                const int r = p >> 2, k = (p & 3) * 4;
+                sm.a[buf][k][r] = ra[i].x;
+                sm.a[buf][k + 1][r] = ra[i].y;
+                sm.a[buf][k + 2][r] = ra[i].z;
+                sm.a[buf][k + 3][r] = ra[i].w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = tid + i * kThreads;
+            if (kOp == kFfnGrad || kOp == kFfnDx) {
+                const int n = p >> 2, k = (p & 3) * 4;
+                sm.b[buf][k][n] = rb[i].x;
+                sm.b[buf][k + 1][n] = rb[i].y;
+                sm.b[buf][k + 2][n] = rb[i].z;
+                sm.b[buf][k + 3][n] = rb[i].w;
+            } else {
+                *reinterpret_cast<float4*>(&sm.b[buf][p >> 5][(p & 31) * 4]) = rb[i];
+            }
+        }
+    };
+
+    float acc[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+
+    const int64_t chunks = (K + kK - 1) / kK;
+    if (chunks > 0) {
+        fetch(0);
+        put(0);
+    }
+    __syncthreads();
+    for (int64_t c = 0; c < chunks; ++c) {
+        const int buf = static_cast<int>(c & 1);
+        if (c + 1 < chunks) fetch((c + 1) * kK);
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+            const float4 a0 = *reinterpret_cast<const float4*>(&sm.a[buf][k][ty * 8]);
+            const float4 a1 = *reinterpret_cast<const float4*>(&sm.a[buf][k][ty * 8 + 4]);
+            const float4 b0 = *reinterpret_cast<const float4*>(&sm.b[buf][k][tx * 4]);
+            const float4 b1 = *reinterpret_cast<const float4*>(&sm.b[buf][k][64 + tx * 4]);
+            const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+            const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+        }
+        if (c + 1 < chunks) put(buf ^ 1);
+        __syncthreads();
+    }
+
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = ty * 8 + i;
+        if (r >= rows) continue;
+        const int64_t row = static_cast<int64_t>(row0) + r;
+        const float* v = acc[i];
+        if (kOp == kFfnUp) {
+            const int64_t at = row * F + col[0] + tx * 4;
+            float h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = v[j] / (1.f + expf(-v[j])) * v[4 + j];
+            store4<T>(g.h, at, h[0], h[1], h[2], h[3]);
+            if (g.gate) {
+                store4<T>(g.gate, at, v[0], v[1], v[2], v[3]);
+                store4<T>(g.up, at, v[4], v[5], v[6], v[7]);
+            }
+        } else {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int c = col[half] + tx * 4;
+                if (c >= cols) continue;
+                const float* u = v + 4 * half;
+                if (kOp == kFfnGrad) {
+                    const int64_t at = row * F + c;
+                    const float4 a4 = load4<T>(g.gate, at), b4 = load4<T>(g.up, at);
+                    const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+                    float da[4], db[4], h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float s = 1.f / (1.f + expf(-a[j]));
+                        h[j] = a[j] * s * b[j];
+                        db[j] = u[j] * a[j] * s;
+                        da[j] = u[j] * b[j] * s * (1.f + a[j] * (1.f - s));
+                    }
+                    store4<T>(g.da, at, da[0], da[1], da[2], da[3]);
+                    store4<T>(g.db, at, db[0], db[1], db[2], db[3]);
+                    store4<T>(g.h, at, h[0], h[1], h[2], h[3]);
+                } else if (kOp == kFfnDw) {
+                    void* out = dw2 ? g.dw2 : (half ? g.dw3 : g.dw1);
+                    store4<T>(out, w_at + row * cols + c, u[0], u[1], u[2], u[3]);
+                } else {
+                    store4<T>(kOp == kFfnDown ? g.y : g.dx, row * d + c, u[0], u[1], u[2], u[3]);
+                }
+            }
+        }
+    }
+    griddep_launch_dependents();
+}
+
+template <typename T>
+static cudaError_t launch(int op, const FfnArgs& a, cudaStream_t st) {
+    const unsigned blocks = static_cast<unsigned>((a.R + kM - 1) / kM + a.n);
+    const unsigned fd = static_cast<unsigned>((a.d + kN - 1) / kN), ff = static_cast<unsigned>((a.F + kN - 1) / kN);
+    switch (op) {
+        case kFfnUp:
+            return launch_k(ffn_simt_kernel<T, kFfnUp>, dim3(blocks, a.F / 64), dim3(kThreads), 0, st, a);
+        case kFfnDown:
+            return launch_k(ffn_simt_kernel<T, kFfnDown>, dim3(blocks, fd), dim3(kThreads), 0, st, a);
+        case kFfnGrad:
+            return launch_k(ffn_simt_kernel<T, kFfnGrad>, dim3(blocks, ff), dim3(kThreads), 0, st, a);
+        case kFfnDx:
+            return launch_k(ffn_simt_kernel<T, kFfnDx>, dim3(blocks, fd), dim3(kThreads), 0, st, a);
+        case kFfnDw: {
+            const unsigned tiles = static_cast<unsigned>(a.d / kM) * (a.F / 64) + static_cast<unsigned>(a.F / kM) * fd;
+            return launch_k(ffn_simt_kernel<T, kFfnDw>, dim3(tiles, a.n), dim3(kThreads), 0, st, a);
+        }
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_ffn_simt(int op, bool bf16, const FfnArgs& a, cudaStream_t st) {
+    return bf16 ? launch<uint16_t>(op, a, st) : launch<float>(op, a, st);
+}
+
+}  // namespace moe

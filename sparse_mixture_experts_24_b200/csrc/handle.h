@@ -1,0 +1,46 @@
+// handle.h -- the part of a moe_handle that the feed-forward block and the
+// MXFP4 product (ffn_api.cu) use; moe_api.cu owns the handle and its forward
+// workspace.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <vector>
+
+#include "../../include/moe.h"
+
+namespace moe {
+
+// Workspace of the feed-forward block.  Buffers grow, but a buffer that a
+// larger one replaces stays allocated until moe_destroy: kernels in flight and
+// captured graphs may still use it.  The status word never moves.
+struct FfnWorkspace {
+    int* status = nullptr;
+    void* maps = nullptr;      // device tensor maps of the weight gradients
+    void* h = nullptr;         // [rows][F]
+    int64_t h_rows = 0;
+    void* da = nullptr;        // [grad_rows][F]
+    void* db = nullptr;
+    int64_t grad_rows = 0;
+    std::vector<void*> allocations;
+};
+
+}  // namespace moe
+
+namespace moe_api_detail {
+
+struct HandleView {
+    int n, d, F;
+    bool bf16;
+    int num_sms;
+    int64_t* launches;
+    moe::FfnWorkspace* ffn;
+};
+
+// Checks the device as every call does and describes the handle.
+moe_status open_handle(moe_handle* h, HandleView* v);
+moe_status failed(moe_status s, const char* fmt, ...);  // sets moe_last_error()
+moe_status done();
+
+}  // namespace moe_api_detail

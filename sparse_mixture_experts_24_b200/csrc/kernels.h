@@ -42,6 +42,7 @@ enum : int {
     kStatusTimeoutDrain = 8,     // waited too long while draining at exit
     kStatusSelfTest = 16,        // the self-test's wait ran out (as it should)
     kStatusEpPlan = 32,          // expert-parallel counts disagree, or a receive buffer is too small
+    kStatusOffsets = 64,         // segment offsets do not ascend within [0, rows]
 };
 
 constexpr int kTcBM = 128;
@@ -363,5 +364,45 @@ cudaError_t launch_tc_gemm1_pair_e4m3(const CUtensorMap& tm_x8, const CUtensorMa
                                       cudaStream_t st);
 cudaError_t launch_tc_gemm2_pair_e4m3(const CUtensorMap& tm_h8, const CUtensorMap& tm_q2, const TcGemmArgs& a,
                                       int num_sms, cudaStream_t st);
+
+// The gated feed-forward block over expert segments, forward and backward
+// (ffn.cuh has the formulas).  Row-major: x, dy, y, dx [R][d]; gate, up, h, da,
+// db [R][F]; w1, w3, dw1, dw3 [n][d][F]; w2, dw2 [n][F][d]; all of one type.
+// offsets: n + 1 device integers, or null (n = 1: all rows).
+enum FfnOp { kFfnUp, kFfnDown, kFfnGrad, kFfnDx, kFfnDw };
+struct FfnArgs {
+    const int32_t* offsets;
+    int n;
+    int64_t R;
+    int d, F;
+    const void *x, *dy, *w1, *w3, *w2;
+    void *gate, *up;  // kFfnUp: written unless null; kFfnGrad: read
+    void *h, *da, *db;
+    void *y, *dx, *dw1, *dw3, *dw2;
+    int* status;
+};
+cudaError_t launch_ffn_simt(int op, bool bf16, const FfnArgs& a, cudaStream_t st);
+
+// MXFP4 (mxfp4.cu): codes [..][K/2] and E8M0 scales [..][K/32], blocks of 32
+// along K; values (the type of the source), if given, receives what they stand
+// for.  Rows: src [rows][cols], blocks along the columns.  Weights: w
+// [n][rows][cols], blocks along the rows, outputs [n][cols][rows ..].
+cudaError_t launch_mx_rows(const void* src, bool bf16, int64_t rows, int cols, uint8_t* codes, uint8_t* scales,
+                           void* values, int num_sms, cudaStream_t st);
+cudaError_t launch_mx_weights(const void* w, bool bf16, int n, int rows, int cols, uint8_t* codes, uint8_t* scales,
+                              void* values, cudaStream_t st);
+
+// Grouped MXFP4 product (gemm_mxfp4.cu): out [R][N] of rows A [R][K] with W
+// [n][N][K] of their expert; b2: the second matrix of the gated pair, or null.
+struct MxGemmArgs {
+    const int32_t* offsets;  // n + 1 device integers, or null (n = 1: all rows)
+    int n;
+    int64_t R;
+    int N, K;
+    const uint8_t *a_codes, *a_scales, *b_codes, *b_scales, *b2_codes, *b2_scales;
+    void* out;
+    int* status;
+};
+cudaError_t launch_mx_gemm(const MxGemmArgs& a, bool bf16_out, int num_sms, cudaStream_t st);
 
 }  // namespace moe

@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "../../include/moe.h"
+#include "handle.h"
 #include "kernels.h"
 
 namespace {
@@ -50,6 +51,16 @@ bool pdl_enabled() {
 namespace moe_api_detail {
 // Lets other translation units of the library set the moe_last_error() text.
 void set_last_error(const char* msg) { snprintf(g_err, sizeof g_err, "%s", msg); }
+
+moe_status failed(moe_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+moe_status done() { return ok(); }
 }  // namespace moe_api_detail
 
 namespace {
@@ -268,6 +279,8 @@ struct moe_handle {
     int trace_max = 0;
     int trace_calls = 0;
     bool tracing = false;
+    // the feed-forward block over expert segments (ffn_api.cu)
+    moe::FfnWorkspace ffn;
 
     size_t esize() const { return dtype == MOE_BF16 ? 2 : 4; }
     size_t osize() const { return dtype == MOE_BF16 ? 2 : 4; }
@@ -322,6 +335,19 @@ moe_status check_device(moe_handle* h) {
     }
     return MOE_OK;
 }
+
+}  // namespace
+
+namespace moe_api_detail {
+moe_status open_handle(moe_handle* h, HandleView* v) {
+    moe_status s = check_device(h);
+    if (s != MOE_OK) return s;
+    *v = HandleView{h->n, h->d, h->F, h->dtype == MOE_BF16, h->num_sms, &h->launches, &h->ffn};
+    return MOE_OK;
+}
+}  // namespace moe_api_detail
+
+namespace {
 
 // Workspace for T tokens and at least rows_min expert rows (T*K for
 // token-choice calls, n*C for expert-choice calls).  Capacities only grow.
@@ -1741,12 +1767,18 @@ moe_status moe_sync_status(moe_handle* h, moe_stream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "pending CUDA error");
-    if (!h->status) return ok();
     int st = 0;
-    e = cudaMemcpy(&st, h->status, sizeof st, cudaMemcpyDeviceToHost);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(status)");
+    for (int* word : {h->status, h->ffn.status}) {
+        if (!word) continue;
+        int v = 0;
+        e = cudaMemcpy(&v, word, sizeof v, cudaMemcpyDeviceToHost);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(status)");
+        if (v != 0) cudaMemset(word, 0, sizeof v);
+        st |= v;
+    }
     if (st != 0) {
-        cudaMemset(h->status, 0, sizeof st);
+        if (st == moe::kStatusOffsets)
+            return fail(MOE_ERR_INVALID_ARG, "segment offsets do not ascend within [0, R] (status bits 0x%x)", st);
         if (st == moe::kStatusEpPlan)
             return fail(MOE_ERR_INVALID_ARG,
                         "expert-parallel plan rejected: counts_all disagrees with this rank's routing or holds a "
@@ -1827,6 +1859,7 @@ moe_status moe_destroy(moe_handle* h) {
     if (!h) return ok();
     trace_free(h);
     if (h->ws) cudaFree(h->ws);
+    for (void* p : h->ffn.allocations) cudaFree(p);
     delete h;
     return ok();
 }
