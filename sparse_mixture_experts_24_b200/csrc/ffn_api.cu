@@ -74,11 +74,12 @@ moe_status need(const HandleView& v, int64_t rows, bool backward, cudaStream_t s
     moe::FfnWorkspace* w = v.ffn;
     if (!w->status) {
         void* p = nullptr;
-        moe_status s = allocate(w, 256, st, use_stream, &p);
+        moe_status s = allocate(w, 256 + sizeof(CUtensorMap) * moe::kFfnDwMaps * v.n, st, use_stream, &p);
         if (s != MOE_OK) return s;
         cudaError_t e = cudaMemset(p, 0, 256);
         if (e != cudaSuccess) return cuda_failed(e, "cudaMemset(status)");
         w->status = static_cast<int*>(p);
+        w->maps = static_cast<uint8_t*>(p) + 256;
     }
     const size_t row = static_cast<size_t>(v.F) * (v.bf16 ? 2 : 4);
     if (rows > w->h_rows) {
@@ -111,9 +112,76 @@ moe::FfnArgs ffn_args(const HandleView& v, int64_t R, const int32_t* offsets) {
     return a;
 }
 
+using moe_api_detail::encode_bf16;
+
+// Row operand [rows][cols]: 128 rows x 64 columns per copy.
+bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int cols) {
+    const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(cols) * 2};
+    const uint32_t box[2] = {64, 128};
+    return encode_bf16(m, p, 2, dims, strides, box);
+}
+
+// Rows [rows][cols] read along their columns: two 64-column chunks of 64 rows.
+bool map_rows_across(CUtensorMap* m, const void* p, int64_t rows, int cols) {
+    const uint64_t dims[3] = {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols) / 64};
+    const uint64_t strides[2] = {static_cast<uint64_t>(cols) * 2, 128};
+    const uint32_t box[3] = {64, 64, 2};
+    return encode_bf16(m, p, 3, dims, strides, box);
+}
+
+// Weights [n][rows][cols] whose rows are the reduction: two 64-column chunks of
+// 64 rows; or whose columns are: 128 rows x 64 columns.
+bool map_weights_across(CUtensorMap* m, const void* p, int n, int rows, int cols) {
+    const uint64_t r = rows, c = cols;
+    const uint64_t dims[4] = {64, r, c / 64, static_cast<uint64_t>(n)};
+    const uint64_t strides[3] = {c * 2, 128, r * c * 2};
+    const uint32_t box[4] = {64, 64, 2, 1};
+    return encode_bf16(m, p, 4, dims, strides, box);
+}
+bool map_weights(CUtensorMap* m, const void* p, int n, int rows, int cols) {
+    const uint64_t r = rows, c = cols;
+    const uint64_t dims[3] = {c, r, static_cast<uint64_t>(n)};
+    const uint64_t strides[2] = {c * 2, r * c * 2};
+    const uint32_t box[3] = {64, 128, 1};
+    return encode_bf16(m, p, 3, dims, strides, box);
+}
+
 moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t st, const char* what) {
-    cudaError_t e = moe::launch_ffn_simt(op, v.bf16, a, st);
+    cudaError_t e;
+    if (v.bf16) {
+        CUtensorMap m[4] = {};
+        const int n = v.n, d = v.d, F = v.F;
+        bool ok = true;
+        if (op == moe::kFfnUp)
+            ok = map_rows(&m[0], a.x, a.R, d) && map_weights_across(&m[2], a.w1, n, d, F) &&
+                 map_weights_across(&m[3], a.w3, n, d, F);
+        else if (op == moe::kFfnDown)
+            ok = map_rows(&m[0], a.h, a.R, F) && map_weights_across(&m[2], a.w2, n, F, d);
+        else if (op == moe::kFfnGrad)
+            ok = map_rows(&m[0], a.dy, a.R, d) && map_weights(&m[2], a.w2, n, F, d);
+        else if (op == moe::kFfnDx)
+            ok = map_rows(&m[0], a.da, a.R, F) && map_rows(&m[1], a.db, a.R, F) &&
+                 map_weights(&m[2], a.w1, n, d, F) && map_weights(&m[3], a.w3, n, d, F);
+        if (!ok) return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%s)", what);
+        e = moe::launch_ffn_tc(op, m, a, v.ffn->maps, v.num_sms, st);
+    } else {
+        e = moe::launch_ffn_simt(op, a, st);
+    }
     if (e != cudaSuccess) return cuda_failed(e, what);
+    *v.launches += 1;
+    return MOE_OK;
+}
+
+// The tensor maps of the weight gradients, one set per expert, on the device.
+moe_status run_maps(const HandleView& v, const moe::FfnArgs& a, cudaStream_t st) {
+    CUtensorMap m[moe::kFfnDwMaps];
+    if (!map_rows_across(&m[0], a.x, a.R, v.d) || !map_rows_across(&m[1], a.h, a.R, v.F) ||
+        !map_rows_across(&m[2], a.da, a.R, v.F) || !map_rows_across(&m[3], a.db, a.R, v.F) ||
+        !map_rows_across(&m[4], a.dy, a.R, v.d))
+        return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (weight gradients)");
+    cudaError_t e = moe::launch_ffn_maps(m, a.offsets, v.n, a.R, v.ffn->maps, a.status, st);
+    if (e != cudaSuccess) return cuda_failed(e, "tensor map launch");
     *v.launches += 1;
     return MOE_OK;
 }
@@ -229,7 +297,8 @@ moe_status moe_ffn_backward(moe_handle* h, int64_t R, const int32_t* offsets, co
     a.dw3 = dw3;
     a.dw2 = dw2;
     moe::chain_begin();
-    s = run(v, moe::kFfnGrad, a, st, "feed-forward hidden gradient launch");
+    if (dw1 && v.bf16) s = run_maps(v, a, st);
+    if (s == MOE_OK) s = run(v, moe::kFfnGrad, a, st, "feed-forward hidden gradient launch");
     if (s == MOE_OK && dx) s = run(v, moe::kFfnDx, a, st, "feed-forward input gradient launch");
     if (s == MOE_OK && dw1) s = run(v, moe::kFfnDw, a, st, "feed-forward weight gradient launch");
     return s == MOE_OK ? done() : s;

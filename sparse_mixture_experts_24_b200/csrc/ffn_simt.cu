@@ -1,5 +1,6 @@
 // ffn_simt.cu -- the gated feed-forward block over expert segments, forward
-// and backward, on the CUDA cores: fp32 multiply-adds for both types.
+// and backward, in fp32 on the CUDA cores (tensor cores have no fp32 x fp32
+// kind that keeps full fp32 products).
 //
 // Five products share one kernel (ffn.cuh has the formulas):
 //   kFfnUp    [a | b] = x . [w1 | w3] -> h (and a, b when they are kept)
@@ -25,30 +26,11 @@ namespace ffn_simt {
 
 constexpr int kM = 64, kN = 128, kK = 16, kThreads = 128;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const void* p, int64_t i);
-template <>
-__device__ __forceinline__ float4 load4<float>(const void* p, int64_t i) {
+__device__ __forceinline__ float4 load4(const void* p, int64_t i) {
     return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
 }
-template <>
-__device__ __forceinline__ float4 load4<uint16_t>(const void* p, int64_t i) {
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
-    float4 v;
-    unpack_bf16x2(q.x, v.x, v.y);
-    unpack_bf16x2(q.y, v.z, v.w);
-    return v;
-}
-
-template <typename T>
-__device__ __forceinline__ void store4(void* p, int64_t i, float a, float b, float c, float d);
-template <>
-__device__ __forceinline__ void store4<float>(void* p, int64_t i, float a, float b, float c, float d) {
+__device__ __forceinline__ void store4(void* p, int64_t i, float a, float b, float c, float d) {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(a, b, c, d);
-}
-template <>
-__device__ __forceinline__ void store4<uint16_t>(void* p, int64_t i, float a, float b, float c, float d) {
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
 struct __align__(16) Smem {
@@ -62,7 +44,7 @@ static_assert((kM + 4) % 4 == 0 && (kN + 4) % 4 == 0 && offsetof(Smem, b) % 16 =
 
 using namespace ffn_simt;
 
-template <typename T, int kOp>
+template <int kOp>
 __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
     griddep_wait();
     __shared__ Smem sm;
@@ -111,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
             if (kOp == kFfnDw) {  // A(m, k) = row k of x (or h), feature m: 16 pieces of a row
                 const int64_t k = k0 + (p >> 4);
                 const int m = row0 + (p & 15) * 4;
-                ra[i] = k < K ? (dw2 ? load4<T>(g.h, (seg0 + k) * F + m) : load4<T>(g.x, (seg0 + k) * d + m)) : zero;
+                ra[i] = k < K ? (dw2 ? load4(g.h, (seg0 + k) * F + m) : load4(g.x, (seg0 + k) * d + m)) : zero;
             } else {
                 const int r = p >> 2;
                 const int64_t k = k0 + (p & 3) * 4;
@@ -119,13 +101,13 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
                 if (r >= rows)
                     ra[i] = zero;
                 else if (kOp == kFfnUp)
-                    ra[i] = load4<T>(g.x, row * d + k);
+                    ra[i] = load4(g.x, row * d + k);
                 else if (kOp == kFfnDown)
-                    ra[i] = load4<T>(g.h, row * F + k);
+                    ra[i] = load4(g.h, row * F + k);
                 else if (kOp == kFfnGrad)
-                    ra[i] = load4<T>(g.dy, row * d + k);
+                    ra[i] = load4(g.dy, row * d + k);
                 else
-                    ra[i] = k < F ? load4<T>(g.da, row * F + k) : load4<T>(g.db, row * F + k - F);
+                    ra[i] = k < F ? load4(g.da, row * F + k) : load4(g.db, row * F + k - F);
             }
         }
 #pragma unroll
@@ -138,9 +120,9 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
                 if (c >= cols)
                     rb[i] = zero;
                 else if (kOp == kFfnGrad)
-                    rb[i] = load4<T>(g.w2, w_at + c * d + k);
+                    rb[i] = load4(g.w2, w_at + c * d + k);
                 else
-                    rb[i] = k < F ? load4<T>(g.w1, w_at + c * F + k) : load4<T>(g.w3, w_at + c * F + k - F);
+                    rb[i] = k < F ? load4(g.w1, w_at + c * F + k) : load4(g.w3, w_at + c * F + k - F);
             } else {  // n contiguous
                 const int64_t k = k0 + (p >> 5);
                 const int n = (p & 31) * 4, half = n >> 6;
@@ -148,13 +130,13 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
                 if (c >= cols || k >= K)
                     rb[i] = zero;
                 else if (kOp == kFfnUp)
-                    rb[i] = load4<T>(half ? g.w3 : g.w1, w_at + k * F + c);
+                    rb[i] = load4(half ? g.w3 : g.w1, w_at + k * F + c);
                 else if (kOp == kFfnDown)
-                    rb[i] = load4<T>(g.w2, w_at + k * d + c);
+                    rb[i] = load4(g.w2, w_at + k * d + c);
                 else if (dw2)
-                    rb[i] = load4<T>(g.dy, (seg0 + k) * d + c);
+                    rb[i] = load4(g.dy, (seg0 + k) * d + c);
                 else
-                    rb[i] = load4<T>(half ? g.db : g.da, (seg0 + k) * F + c);
+                    rb[i] = load4(half ? g.db : g.da, (seg0 + k) * F + c);
             }
         }
     };
@@ -230,10 +212,10 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
             float h[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) h[j] = v[j] / (1.f + expf(-v[j])) * v[4 + j];
-            store4<T>(g.h, at, h[0], h[1], h[2], h[3]);
+            store4(g.h, at, h[0], h[1], h[2], h[3]);
             if (g.gate) {
-                store4<T>(g.gate, at, v[0], v[1], v[2], v[3]);
-                store4<T>(g.up, at, v[4], v[5], v[6], v[7]);
+                store4(g.gate, at, v[0], v[1], v[2], v[3]);
+                store4(g.up, at, v[4], v[5], v[6], v[7]);
             }
         } else {
 #pragma unroll
@@ -243,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
                 const float* u = v + 4 * half;
                 if (kOp == kFfnGrad) {
                     const int64_t at = row * F + c;
-                    const float4 a4 = load4<T>(g.gate, at), b4 = load4<T>(g.up, at);
+                    const float4 a4 = load4(g.gate, at), b4 = load4(g.up, at);
                     const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
                     float da[4], db[4], h[4];
 #pragma unroll
@@ -253,14 +235,14 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
                         db[j] = u[j] * a[j] * s;
                         da[j] = u[j] * b[j] * s * (1.f + a[j] * (1.f - s));
                     }
-                    store4<T>(g.da, at, da[0], da[1], da[2], da[3]);
-                    store4<T>(g.db, at, db[0], db[1], db[2], db[3]);
-                    store4<T>(g.h, at, h[0], h[1], h[2], h[3]);
+                    store4(g.da, at, da[0], da[1], da[2], da[3]);
+                    store4(g.db, at, db[0], db[1], db[2], db[3]);
+                    store4(g.h, at, h[0], h[1], h[2], h[3]);
                 } else if (kOp == kFfnDw) {
                     void* out = dw2 ? g.dw2 : (half ? g.dw3 : g.dw1);
-                    store4<T>(out, w_at + row * cols + c, u[0], u[1], u[2], u[3]);
+                    store4(out, w_at + row * cols + c, u[0], u[1], u[2], u[3]);
                 } else {
-                    store4<T>(kOp == kFfnDown ? g.y : g.dx, row * d + c, u[0], u[1], u[2], u[3]);
+                    store4(kOp == kFfnDown ? g.y : g.dx, row * d + c, u[0], u[1], u[2], u[3]);
                 }
             }
         }
@@ -268,29 +250,24 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
     griddep_launch_dependents();
 }
 
-template <typename T>
-static cudaError_t launch(int op, const FfnArgs& a, cudaStream_t st) {
+cudaError_t launch_ffn_simt(int op, const FfnArgs& a, cudaStream_t st) {
     const unsigned blocks = static_cast<unsigned>((a.R + kM - 1) / kM + a.n);
     const unsigned fd = static_cast<unsigned>((a.d + kN - 1) / kN), ff = static_cast<unsigned>((a.F + kN - 1) / kN);
     switch (op) {
         case kFfnUp:
-            return launch_k(ffn_simt_kernel<T, kFfnUp>, dim3(blocks, a.F / 64), dim3(kThreads), 0, st, a);
+            return launch_k(ffn_simt_kernel<kFfnUp>, dim3(blocks, a.F / 64), dim3(kThreads), 0, st, a);
         case kFfnDown:
-            return launch_k(ffn_simt_kernel<T, kFfnDown>, dim3(blocks, fd), dim3(kThreads), 0, st, a);
+            return launch_k(ffn_simt_kernel<kFfnDown>, dim3(blocks, fd), dim3(kThreads), 0, st, a);
         case kFfnGrad:
-            return launch_k(ffn_simt_kernel<T, kFfnGrad>, dim3(blocks, ff), dim3(kThreads), 0, st, a);
+            return launch_k(ffn_simt_kernel<kFfnGrad>, dim3(blocks, ff), dim3(kThreads), 0, st, a);
         case kFfnDx:
-            return launch_k(ffn_simt_kernel<T, kFfnDx>, dim3(blocks, fd), dim3(kThreads), 0, st, a);
+            return launch_k(ffn_simt_kernel<kFfnDx>, dim3(blocks, fd), dim3(kThreads), 0, st, a);
         case kFfnDw: {
             const unsigned tiles = static_cast<unsigned>(a.d / kM) * (a.F / 64) + static_cast<unsigned>(a.F / kM) * fd;
-            return launch_k(ffn_simt_kernel<T, kFfnDw>, dim3(tiles, a.n), dim3(kThreads), 0, st, a);
+            return launch_k(ffn_simt_kernel<kFfnDw>, dim3(tiles, a.n), dim3(kThreads), 0, st, a);
         }
     }
     return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_ffn_simt(int op, bool bf16, const FfnArgs& a, cudaStream_t st) {
-    return bf16 ? launch<uint16_t>(op, a, st) : launch<float>(op, a, st);
 }
 
 }  // namespace moe

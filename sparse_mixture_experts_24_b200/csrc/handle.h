@@ -3,6 +3,7 @@
 // workspace.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -40,6 +41,10 @@ struct HandleView {
 
 // Checks the device as every call does and describes the handle.
 moe_status open_handle(moe_handle* h, HandleView* v);
+// bf16 tensor map with 128-byte swizzle: dims and box from the contiguous axis
+// outwards, strides of the axes after the first in bytes.
+bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                 const uint32_t* box);
 moe_status failed(moe_status s, const char* fmt, ...);  // sets moe_last_error()
 moe_status done();
 

@@ -381,7 +381,31 @@ struct FfnArgs {
     void *y, *dx, *dw1, *dw3, *dw2;
     int* status;
 };
-cudaError_t launch_ffn_simt(int op, bool bf16, const FfnArgs& a, cudaStream_t st);
+// fp32 on the CUDA cores (ffn_simt.cu).
+cudaError_t launch_ffn_simt(int op, const FfnArgs& a, cudaStream_t st);
+
+// bf16 on the tensor cores (gemm_ffn.cu).  maps: A (and A2), B (and B2) of the
+// op -- row operands [R][cols] in 64 x 128 boxes; weights that are N-major
+// ([n][K][N], kFfnUp and kFfnDown) as 4-D maps (64 columns, rows, 64-column
+// chunk, expert) in boxes of 64 rows and two chunks; weights that are K-major
+// ([n][N][K], kFfnGrad and kFfnDx) as 3-D maps in 64 x 128 boxes.  kFfnDw
+// takes its operands from the maps that launch_ffn_maps has written to device
+// memory: [5][n], of x, h, da, db, dy as 3-D maps (64 columns, rows, 64-column
+// chunk) in boxes of 64 rows and two chunks.
+constexpr int kFfnDwMaps = 5;
+struct FfnTcArgs {
+    FfnArgs f;
+    int n, d, F;
+    int steps;    // 64-deep K steps (row ops)
+    int n_tiles;  // column tiles (row ops)
+    int band;     // row blocks per band of the tile order
+    int dw_tiles13, dw_tiles2;
+    const CUtensorMap* maps;
+};
+cudaError_t launch_ffn_maps(const CUtensorMap* maps5, const int32_t* offsets, int n, int64_t R, void* out,
+                            int* status, cudaStream_t st);
+cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnArgs& f, const void* dw_maps, int num_sms,
+                          cudaStream_t st);
 
 // MXFP4 (mxfp4.cu): codes [..][K/2] and E8M0 scales [..][K/32], blocks of 32
 // along K; values (the type of the source), if given, receives what they stand
