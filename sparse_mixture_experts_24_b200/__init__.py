@@ -13,6 +13,7 @@ Up Two Specialists").
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -431,25 +432,39 @@ def _take(where: str, name: str, t, dtype, shape):
     """Refuse a tensor that the C ABI would misread: `t` has to be a contiguous
     CUDA tensor of this type and shape on the current device."""
     import torch
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == torch.cuda.current_device()):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _refuse(where, "%s is not a CUDA tensor" % name)
     if t.dtype != dtype:
         _refuse(where, "%s is %s, not %s" % (name, t.dtype, dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         _refuse(where, "%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_contiguous():
         _refuse(where, "%s is not contiguous" % name)
-    if t.device.index != torch.cuda.current_device():
-        _refuse(where, "%s is on %s, the current device is %d" % (name, t.device, torch.cuda.current_device()))
+    _refuse(where, "%s is on %s, the current device is %d" % (name, t.device, torch.cuda.current_device()))
+
+
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def _on(stream):
     """Context in which outputs are allocated: the stream the kernels run on,
     so that the allocator does not hand out memory still in use there."""
-    import torch
     if stream is None:
-        return torch.cuda.stream(torch.cuda.current_stream())
+        return _NO_CONTEXT
+    import torch
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+def _call_stream(s):
+    """Handle of the stream to launch on, for calls whose tensors _take has
+    already found on the current CUDA device."""
+    if s is None:
+        import torch
+        return torch.cuda.current_stream().cuda_stream
+    return _stream(s)
 
 
 def _mx_dtype(where: str, name: str, t):
@@ -471,12 +486,12 @@ def quantize_mxfp4(x, values: bool = False, stream=None):
     if x.dim() < 1 or x.shape[-1] < 32 or x.shape[-1] % 32:
         _refuse(where, "x has shape %s: the last dimension must be a positive multiple of 32" % (tuple(x.shape),))
     _take(where, "x", x, x.dtype, x.shape)
-    cols = x.shape[-1]
+    cols, lead = x.shape[-1], x.shape[:-1]
     with _on(stream):
-        codes = torch.empty(*x.shape[:-1], cols // 2, dtype=torch.uint8, device=x.device)
-        scales = torch.empty(*x.shape[:-1], cols // 32, dtype=torch.uint8, device=x.device)
+        codes = torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((*lead, cols // 32), dtype=torch.uint8, device=x.device)
         v = torch.empty_like(x) if values else None
-    moe_quantize_mxfp4(x.numel() // cols, cols, x, dt, codes, scales, v, stream)
+    moe_quantize_mxfp4(x.numel() // cols, cols, x, dt, codes, scales, v, _call_stream(stream))
     return (codes, scales, v) if values else (codes, scales)
 
 
@@ -496,7 +511,7 @@ def quantize_weights_mxfp4(w, values: bool = False, stream=None):
         codes = torch.empty(n, cols, rows // 2, dtype=torch.uint8, device=w.device)
         scales = torch.empty(n, cols, rows // 32, dtype=torch.uint8, device=w.device)
         v = torch.empty(n, cols, rows, dtype=w.dtype, device=w.device) if values else None
-    moe_quantize_weights_mxfp4(n, rows, cols, w, dt, codes, scales, v, stream)
+    moe_quantize_weights_mxfp4(n, rows, cols, w, dt, codes, scales, v, _call_stream(stream))
     return (codes, scales, v) if values else (codes, scales)
 
 
@@ -666,7 +681,7 @@ class MoELayer:
             gate = torch.empty(R, self.ffn, dtype=x.dtype, device=x.device) if keep else None
             up = torch.empty_like(gate) if keep else None
         _take(where, "y", y, x.dtype, x.shape)
-        moe_ffn_forward(self.h, R, offsets, x, w1, w3, w2, gate, up, y, stream)
+        moe_ffn_forward(self.h, R, offsets, x, w1, w3, w2, gate, up, y, _call_stream(stream))
         return (y, gate, up) if keep else y
 
     def ffn_backward(self, dy, x, gate, up, w1, w3, w2, offsets=None, need_dx: bool = True, need_dw: bool = True,
@@ -683,7 +698,7 @@ class MoELayer:
         with _on(stream):
             dx = torch.empty_like(x) if need_dx else None
             dw = [torch.empty_like(w) if need_dw else None for w in (w1, w3, w2)]
-        moe_ffn_backward(self.h, R, offsets, x, w1, w3, w2, gate, up, dy, dx, *dw, stream)
+        moe_ffn_backward(self.h, R, offsets, x, w1, w3, w2, gate, up, dy, dx, *dw, _call_stream(stream))
         return (dx, *dw)
 
     def matmul_mxfp4(self, a, w, pair=None, offsets=None, out=None, stream=None):
@@ -715,7 +730,7 @@ class MoELayer:
                 out = torch.empty(R, N, dtype=dt, device=a[0].device)
         _take(where, "out", out, dt, (R, N))
         p = pair if pair is not None else (None, None)
-        moe_matmul_mxfp4(self.h, R, N, K, offsets, *a[:2], *w[:2], *p[:2], out, stream)
+        moe_matmul_mxfp4(self.h, R, N, K, offsets, *a[:2], *w[:2], *p[:2], out, _call_stream(stream))
         return out
 
     def set_capacity_factor(self, factor: float) -> None:

@@ -387,8 +387,18 @@ moe_status moe_matmul_mxfp4(moe_handle* h, int64_t R, int N, int K, const int32_
     if (s != MOE_OK) return s;
     moe::MxGemmArgs a{offsets,  v.n,      R,          N,           K,   a_codes,      a_scales,
                       w_codes,  w_scales, pair_codes, pair_scales, out, v.ffn->status};
+    const uint64_t k2 = static_cast<uint64_t>(K) / 2, cols = static_cast<uint64_t>(N);
+    const uint64_t a_dims[2] = {k2, static_cast<uint64_t>(R)}, a_strides[1] = {k2};
+    const uint32_t a_box[2] = {128, static_cast<uint32_t>(moe::mx_gemm_tile_rows(R, v.n))};
+    const uint64_t w_dims[3] = {k2, cols, static_cast<uint64_t>(v.n)}, w_strides[2] = {k2, k2 * cols};
+    const uint32_t w_box[3] = {128, 128, 1};
+    CUtensorMap m[3] = {};
+    if (!moe_api_detail::encode_bytes(&m[0], a_codes, 2, a_dims, a_strides, a_box) ||
+        !moe_api_detail::encode_bytes(&m[1], w_codes, 3, w_dims, w_strides, w_box) ||
+        (pair_codes && !moe_api_detail::encode_bytes(&m[2], pair_codes, 3, w_dims, w_strides, w_box)))
+        return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (MXFP4 product)");
     moe::chain_begin();
-    cudaError_t e = moe::launch_mx_gemm(a, v.bf16, v.num_sms, st);
+    cudaError_t e = moe::launch_mx_gemm(m, a, v.bf16, v.num_sms, st);
     if (e != cudaSuccess) return cuda_failed(e, "MXFP4 product launch");
     *v.launches += 1;
     return done();

@@ -1,118 +1,482 @@
 // gemm_mxfp4.cu -- grouped products of MXFP4 rows with the MXFP4 matrices of
-// their expert:
+// their expert on the sm_100a block-scaled tensor cores:
 //   out[r] = A[r] . W_e^T                              (plain)
-//   out[r] = silu(A[r] . W1_e^T) (*) (A[r] . W3_e^T)   (pair)
-// A [R][K] and W [n][N][K] as codes [..][K/2] and scales [..][K/32] (mxfp4.cu).
+//   out[r] = silu(A[r] . W_e^T) (*) (A[r] . P_e^T)     (pair)
+// A [R][K] and W, P [n][N][K] as codes [..][K/2] and scales [..][K/32]
+// (mxfp4.cu).  tcgen05.mma kind::mxf4 multiplies the E2M1 codes with their
+// power-of-two scales (one per 32 of K) and accumulates in fp32.
 //
-// A block owns 64 rows x 64 columns (of both matrices for a pair), decodes one
-// block of 32 reduction elements at a time into shared memory and multiplies
-// in fp32: 256 threads, 4 x 4 outputs each.
+// One persistent CTA per SM, 384 threads, tiles of kTM rows x kBN columns (a
+// pair: 128 columns of W beside the same 128 of P), K in steps of 256:
+//   warp 0       TMA: codes of the tile's rows and columns (128 bytes per row and
+//                step, 128-byte swizzle; past K, N or R the copy reads zeros);
+//   warps 10-11  scales.  The format keeps a row's scales contiguous, the tensor
+//                core wants, per 128 rows and 128 of K, 512 bytes with row r's
+//                four at 16 (r % 32) + 4 (r / 32): these warps fetch 16 scales (two
+//                steps) of each row at a time, one fetch ahead, and turn them
+//                over on the way into shared memory, so no packed copy of the
+//                scales has to exist anywhere;
+//   warp 1       one thread copies a step's scales into tensor memory
+//                (tcgen05.cp 32x128b.warpx4) and issues its four MMAs (K 64);
+//                a copy holds the scales of two MMAs, told apart by the
+//                descriptor's scale id;
+//   warps 2-9    epilogue, two per 32 accumulator rows, each on half the columns:
+//                the accumulators go to registers and are handed back first.
+// kTM = 32 loads only 32 rows of A per tile (batches of few rows per expert);
+// the MMA's other 96 rows read whatever follows and are never stored.
+// Every wait is bounded (common.cuh).
 #include "ffn.cuh"
 #include "kernels.h"
 
 namespace moe {
 
 namespace mxg {
-constexpr int kM = 64, kN = 64, kThreads = 256;
-struct Smem {
-    SegmentPlan plan;
-    float a[32][kM + 4];
-    float b[2][32][kN + 4];
+
+constexpr int kBK = 256;                    // K per step: 128 bytes of codes
+constexpr int kBBlockBytes = 128 * 128;     // 128 columns
+constexpr int kSfBytes = 2 * 512;           // a step's scales of 128 rows
+constexpr int kTmemCols = 512;
+constexpr int kEpiWarps = 8;
+constexpr int kLoadWarp = 2 + kEpiWarps, kLoadThreads = 64;
+constexpr int kThreads = kLoadWarp * 32 + kLoadThreads;
+constexpr int kMaxStages = 8;
+
+template <int kBN, int kTM>
+struct Cfg {
+    static constexpr int kBlocks = kBN / 128;
+    static constexpr int kABytes = kTM * 128;
+    static constexpr int kCodeBytes = kABytes + kBlocks * kBBlockBytes;
+    static constexpr int kStageBytes = (kCodeBytes + (1 + kBlocks) * kSfBytes + 1023) / 1024 * 1024;
+    static constexpr int kStages = kBN == 128 ? (kTM == 32 ? 8 : 6) : (kTM == 32 ? 5 : 4);
+    static constexpr int kAccBufs = kBN == 128 ? 2 : 1;
+    static constexpr int kSfCols = 8 * (1 + kBlocks);  // per stage
+    static constexpr int kSfBase = kAccBufs * kBN;
+    static constexpr int kRows = kTM + kBN;            // rows whose scales a step needs
+    static constexpr int kPer = (kRows + kLoadThreads - 1) / kLoadThreads;
+    static_assert(kSfBase + kStages * kSfCols <= kTmemCols && kStages <= kMaxStages, "tensor memory");
 };
-__device__ __forceinline__ float value(uint32_t code) {
-    const uint32_t ex = (code >> 1) & 3u, man = code & 1u;
-    const float mag = ex == 0u ? 0.5f * man : __uint_as_float(((ex + 126u) << 23) | (man << 22));
-    return (code & 8u) ? -mag : mag;
+
+struct __align__(16) Tail {
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    uint64_t accum_full[2];
+    uint64_t accum_empty[2];
+    uint64_t done;
+    uint32_t tmem_base;
+    SegmentPlan plan;
+};
+
+template <int kBN, int kTM>
+constexpr int smem_bytes() {
+    return Cfg<kBN, kTM>::kStages * Cfg<kBN, kTM>::kStageBytes + (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128 +
+           1024;
 }
-__device__ __forceinline__ float scale(uint32_t c) {
-    return c == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(c == 0u ? 0x00400000u : c << 23);
+
+struct Tile {
+    int e, n_tile, row0, rows;
+};
+
+// Tile t -> (expert, column tile, row block), the row block fastest: the
+// expert's rows (K / 2 bytes each) stay in L2 while its columns stream past.
+template <int kTM>
+__device__ __forceinline__ Tile tile_at(int t, const SegmentPlan& p, int n, int n_tiles) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.blk[mid] * n_tiles <= t)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int local = t - p.blk[lo] * n_tiles, count = p.blk[lo + 1] - p.blk[lo];
+    Tile ti;
+    ti.e = lo;
+    ti.n_tile = local / count;
+    ti.row0 = p.off[lo] + (local - ti.n_tile * count) * kTM;
+    ti.rows = min(kTM, p.off[lo + 1] - ti.row0);
+    return ti;
 }
+
+// D[tmem] (+)= A x B, E2M1 operands with a power-of-two scale per 32 of K.
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+
+// E2M1 A and B (code 1), E8M0 scales (scale format 1), both K-major; `id`: the
+// byte of each 32-bit scale word where this MMA's two scales start.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t id) {
+    return (id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
+           (static_cast<uint32_t>(M >> 4) << 24) | (id << 29);
+}
+
+// fp32 outputs keep the library exponential (2 ulp); the fast division adds 2
+// ulp and gives 0 for a below -87, where silu is under 1e-35.
+template <bool kBf16Out>
+__device__ __forceinline__ float silu(float a) {
+    return __fdividef(a, 1.f + (kBf16Out ? __expf(-a) : expf(-a)));
+}
+
+// The 16 scales g * 16 .. of one row, zeros (the smallest scale, on codes that
+// are zero too) past the row's nb.  `how`: 4 -- rows are 16-byte aligned and a
+// multiple of 16 long; 2 -- the same for 4; else byte by byte.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int g, int nb, int how) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    const int at = g * 16;
+    if (how == 4) return __ldg(reinterpret_cast<const uint4*>(row + at));
+    if (how == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (at + 4 * i < nb) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + at + 4 * i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (at + i < nb) w[i >> 2] |= static_cast<uint32_t>(__ldg(row + at + i)) << (8 * (i & 3));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Columns col .. col+31 of one row of out.
+template <bool kBf16>
+__device__ __forceinline__ void store_row32(void* out, int64_t row, int N, int col, const uint32_t (&bits)[32]) {
+    auto v = [&](int j) { return __uint_as_float(bits[j]); };
+    const int64_t at = row * N + col;
+    if (kBf16) {
+        uint16_t* o = static_cast<uint16_t*>(out) + at;
+        if (N % 8 == 0 && col + 32 <= N) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                reinterpret_cast<uint4*>(o)[q] =
+                    make_uint4(pack_bf16x2(v(8 * q), v(8 * q + 1)), pack_bf16x2(v(8 * q + 2), v(8 * q + 3)),
+                               pack_bf16x2(v(8 * q + 4), v(8 * q + 5)), pack_bf16x2(v(8 * q + 6), v(8 * q + 7)));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (col + j < N) o[j] = static_cast<uint16_t>(pack_bf16x2(v(j), 0.f));
+        }
+    } else {
+        float* o = static_cast<float*>(out) + at;
+        if (N % 4 == 0 && col + 32 <= N) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                reinterpret_cast<float4*>(o)[q] = make_float4(v(4 * q), v(4 * q + 1), v(4 * q + 2), v(4 * q + 3));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (col + j < N) o[j] = v(j);
+        }
+    }
+}
+
 }  // namespace mxg
 
 using namespace mxg;
 
-template <bool kPair, bool kBf16Out>
-__global__ void __launch_bounds__(kThreads) mx_gemm_simt_kernel(const MxGemmArgs g) {
-    __shared__ Smem sm;
-    load_plan(sm.plan, g.offsets, g.n, g.R, kM, g.status);
-    if (static_cast<int>(blockIdx.x) >= sm.plan.blk[g.n]) return;
-    const int e = plan_expert(sm.plan, g.n, blockIdx.x);
-    const int row0 = sm.plan.off[e] + (static_cast<int>(blockIdx.x) - sm.plan.blk[e]) * kM;
-    const int rows = min(kM, sm.plan.off[e + 1] - row0);
-    const int col0 = blockIdx.y * kN;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int nb = g.K / 32;
-    float acc[kPair ? 2 : 1][4][4] = {};
-    for (int kb = 0; kb < nb; ++kb) {
-        // 4 threads per row, 4 bytes (8 codes) each
-        const int r = tid >> 2, q = tid & 3;
-#pragma unroll
-        for (int m = 0; m < (kPair ? 3 : 2); ++m) {
-            const uint8_t* codes = m == 0 ? g.a_codes : (m == 1 ? g.b_codes : g.b2_codes);
-            const uint8_t* scales = m == 0 ? g.a_scales : (m == 1 ? g.b_scales : g.b2_scales);
-            const bool in = m == 0 ? r < rows : col0 + r < g.N;
-            const int64_t line = m == 0 ? static_cast<int64_t>(row0) + r : static_cast<int64_t>(e) * g.N + col0 + r;
-            uint32_t w = 0u;
-            float s = 0.f;
-            if (in) {
-                w = __ldg(reinterpret_cast<const uint32_t*>(codes + (line * nb + kb) * 16) + q);
-                s = scale(__ldg(scales + line * nb + kb));
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float v = value((w >> (4 * i)) & 0xFu) * s;
-                if (m == 0)
-                    sm.a[8 * q + i][r] = v;
-                else
-                    sm.b[m - 1][8 * q + i][r] = v;
-            }
+template <bool kPair, bool kBf16Out, int kBN, int kTM>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                   const __grid_constant__ CUtensorMap tm_b2, const MxGemmArgs args, const int scales_how) {
+    using C = Cfg<kBN, kTM>;
+    static_assert(!kPair || kBN == 256, "a pair's tile is one block of each matrix");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    Tail* tail = reinterpret_cast<Tail*>(smem + C::kStages * C::kStageBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kColsOut = kPair ? 128 : kBN;  // output columns of a tile
+    const int n_tiles = (args.N + kColsOut - 1) / kColsOut;
+    const int steps = (args.K + kBK - 1) / kBK;
+    const int nb = args.K / 32;
+    int* status = args.status;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(smem_u32(&tail->full[s]), 1 + kLoadThreads);
+            mbar_init(smem_u32(&tail->empty[s]), 1);
         }
-        __syncthreads();
-#pragma unroll 8
-        for (int k = 0; k < 32; ++k) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int p = 0; p < (kPair ? 2 : 1); ++p)
-                        acc[p][i][j] = fmaf(sm.a[k][ty * 4 + i], sm.b[p][k][tx * 4 + j], acc[p][i][j]);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&tail->accum_full[b]), 1);
+            mbar_init(smem_u32(&tail->accum_empty[b]), kEpiWarps);
         }
-        __syncthreads();
+        mbar_init(smem_u32(&tail->done), 1);
+        fence_barrier_init();
+        fence_proxy_async_smem();
     }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tm_a);
+        tma_prefetch_desc(&tm_b);
+        if (kPair) tma_prefetch_desc(&tm_b2);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&tail->tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    griddep_wait();
+    load_plan(tail->plan, args.offsets, args.n, args.R, kTM, status);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = tail->tmem_base;
+    const SegmentPlan& plan = tail->plan;
+    const int total = plan.blk[args.n] * n_tiles;
+    const int first = blockIdx.x, stride = gridDim.x;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer ----------------
+            int stage = 0;
+            uint32_t phase = 0;
+            int armed[kMaxStages];
+            for (int s = 0; s < kMaxStages; ++s) armed[s] = -1;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += stride) {
+                const Tile ti = tile_at<kTM>(t, plan, args.n, n_tiles);
+                for (int ks = 0; ks < steps; ++ks) {
+                    if (!mbar_wait(smem_u32(&tail->empty[stage]), phase ^ 1u, status, kStatusTimeoutEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&tail->full[stage]);
+                    mbar_arrive_expect_tx(fb, C::kCodeBytes);
+                    armed[stage] = static_cast<int>(phase);
+                    const uint32_t base = smem_u32(smem + stage * C::kStageBytes);
+                    tma_load_2d(base, &tm_a, fb, ks * 128, ti.row0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty * 4 + i;
-        if (r >= rows) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = col0 + tx * 4 + j;
-            if (c >= g.N) continue;
-            float v = acc[0][i][j];
-            if (kPair) v = v / (1.f + expf(-v)) * acc[kPair ? 1 : 0][i][j];
-            const int64_t at = (static_cast<int64_t>(row0) + r) * g.N + c;
-            if (kBf16Out)
-                static_cast<uint16_t*>(g.out)[at] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
-            else
-                static_cast<float*>(g.out)[at] = v;
+                    for (int b = 0; b < C::kBlocks; ++b)
+                        tma_load_3d(base + C::kABytes + b * kBBlockBytes, kPair && b == 1 ? &tm_b2 : &tm_b, fb,
+                                    ks * 128, kPair ? ti.n_tile * 128 : ti.n_tile * kBN + b * 128, ti.e);
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // nothing may still be landing when the CTA exits
+            for (int s = 0; s < C::kStages; ++s)
+                if (armed[s] >= 0)
+                    mbar_wait(smem_u32(&tail->full[s]), static_cast<uint32_t>(armed[s]), status, kStatusTimeoutDrain);
         }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- scale copies and MMAs ----------------
+            int stage = 0;
+            uint32_t phase = 0;
+            int local = 0;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += stride, ++local) {
+                const int buf = C::kAccBufs == 2 ? (local & 1) : 0;
+                const uint32_t use = static_cast<uint32_t>(C::kAccBufs == 2 ? local >> 1 : local);
+                if (!mbar_wait(smem_u32(&tail->accum_empty[buf]), (use & 1u) ^ 1u, status, kStatusTimeoutAccum)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * kBN);
+                for (int ks = 0; ks < steps; ++ks) {
+                    if (!mbar_wait(smem_u32(&tail->full[stage]), phase, status, kStatusTimeoutFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t base = smem_u32(smem + stage * C::kStageBytes);
+                    const uint32_t sf_smem = base + C::kCodeBytes;
+                    const uint32_t sf = tmem_base + static_cast<uint32_t>(C::kSfBase + stage * C::kSfCols);
+                    // tensor memory: A's two chunks, then for either chunk the blocks of B
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        tc_cp_32x128b_warpx4(sf + 4 * c, make_smem_desc(sf_smem + c * 512, 0, 128, 0));
+#pragma unroll
+                        for (int b = 0; b < C::kBlocks; ++b)
+                            tc_cp_32x128b_warpx4(sf + 8 + 4 * (c * C::kBlocks + b),
+                                                 make_smem_desc(sf_smem + (1 + b) * kSfBytes + c * 512, 0, 128, 0));
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const int c = kk >> 1;
+                        const uint64_t ad = make_smem_desc(base + kk * 32, 16, 1024, 2);
+                        const uint64_t bd = make_smem_desc(base + C::kABytes + kk * 32, 16, 1024, 2);
+                        mma_mxf4(d_tmem, ad, bd, (kk & 1) ? idesc_mxf4(128, kBN, 2) : idesc_mxf4(128, kBN, 0),
+                                 sf + 4 * c, sf + 8 + 4 * C::kBlocks * c, (ks | kk) != 0 ? 1u : 0u);
+                    }
+                    tc_commit(smem_u32(&tail->empty[stage]));
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) tc_commit(smem_u32(&tail->accum_full[buf]));
+            }
+            // every copy and MMA is done before tensor memory is freed
+            tc_commit(smem_u32(&tail->done));
+            mbar_wait(smem_u32(&tail->done), 0, status, kStatusTimeoutDrain);
+        }
+    } else if (warp >= kLoadWarp) {
+        // ---------------- scales ----------------
+        const int lt = static_cast<int>(threadIdx.x) - kLoadWarp * 32;
+        uint4 cur[C::kPer], next[C::kPer];
+        const int groups = (steps + 1) / 2;  // of two steps
+        auto fetch = [&](int t, int g, uint4 (&to)[C::kPer]) {
+            const Tile ti = tile_at<kTM>(t, plan, args.n, n_tiles);
+#pragma unroll
+            for (int i = 0; i < C::kPer; ++i) {
+                const int r = lt + i * kLoadThreads;
+                const uint8_t* row = nullptr;
+                if (r < kTM) {
+                    if (r < ti.rows) row = args.a_scales + (static_cast<int64_t>(ti.row0) + r) * nb;
+                } else if (r < C::kRows) {
+                    const int j = r - kTM, b = j >> 7;
+                    const int col = kPair ? ti.n_tile * 128 + (j & 127) : ti.n_tile * kBN + j;
+                    if (col < args.N)
+                        row = (kPair && b ? args.b2_scales : args.b_scales) +
+                              (static_cast<int64_t>(ti.e) * args.N + col) * nb;
+                }
+                to[i] = row ? load_scales(row, g, nb, scales_how) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        if (first < total) fetch(first, 0, next);
+        for (int t = first; t < total && ok; t += stride) {
+            for (int g = 0; g < groups && ok; ++g) {
+#pragma unroll
+                for (int i = 0; i < C::kPer; ++i) cur[i] = next[i];
+                if (g + 1 < groups)
+                    fetch(t, g + 1, next);
+                else if (t + stride < total)
+                    fetch(t + stride, 0, next);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (2 * g + s >= steps) break;
+                    if (!mbar_wait(smem_u32(&tail->empty[stage]), phase ^ 1u, status, kStatusTimeoutEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* sf = smem + stage * C::kStageBytes + C::kCodeBytes;
+#pragma unroll
+                    for (int i = 0; i < C::kPer; ++i) {
+                        const int r = lt + i * kLoadThreads;
+                        if (r < C::kRows) {
+                            const int j = r < kTM ? r : (r - kTM) & 127;
+                            const int block = r < kTM ? 0 : 1 + ((r - kTM) >> 7);
+                            uint32_t* dst = reinterpret_cast<uint32_t*>(sf + block * kSfBytes + 16 * (j & 31) +
+                                                                        4 * (j >> 5));
+                            dst[0] = s == 0 ? cur[i].x : cur[i].z;
+                            dst[128] = s == 0 ? cur[i].y : cur[i].w;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(smem_u32(&tail->full[stage]));
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+    } else {
+        // ---------------- epilogue (warps 2..9) ----------------
+        const int quad = warp & 3;         // TMEM lanes 32 * quad .. + 31
+        const int half = (warp - 2) >> 2;  // half of the columns
+        constexpr int kChunks = kBN / 64;  // 32-column chunks per warp
+        int local = 0;
+        for (int t = first; t < total; t += stride, ++local) {
+            const Tile ti = tile_at<kTM>(t, plan, args.n, n_tiles);
+            const int buf = C::kAccBufs == 2 ? (local & 1) : 0;
+            const uint32_t use = static_cast<uint32_t>(C::kAccBufs == 2 ? local >> 1 : local);
+            if (!mbar_wait(smem_u32(&tail->accum_full[buf]), use & 1u, status, kStatusTimeoutAccum)) break;
+            tc_fence_after();
+            const uint32_t tbase =
+                tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(buf * kBN);
+            const bool any = quad * 32 < ti.rows;  // warp-uniform
+            const bool row_ok = quad * 32 + lane < ti.rows;
+            const int64_t row = static_cast<int64_t>(ti.row0) + quad * 32 + lane;
+            uint32_t acc[kChunks][32];
+            if (any) {
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i)
+                    // pair: chunks of W (0, 2) and the same of P (1, 3)
+                    tmem_ld_32x32b_x32(tbase + (kPair ? half * 64 + (i >> 1) * 32 + (i & 1) * 128
+                                                      : (half * kChunks + i) * 32),
+                                       acc[i]);
+                tmem_wait_ld();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&tail->accum_empty[buf]));
+            if (row_ok) {
+#pragma unroll
+                for (int i = 0; i < (kPair ? kChunks / 2 : kChunks); ++i) {
+                    const int col = kPair ? ti.n_tile * 128 + half * 64 + i * 32
+                                          : ti.n_tile * kBN + (half * kChunks + i) * 32;
+                    if (col < args.N) {
+                        uint32_t(&v)[32] = acc[kPair ? 2 * i : i];
+                        if (kPair) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[j] = __float_as_uint(silu<kBf16Out>(__uint_as_float(v[j])) *
+                                                       __uint_as_float(acc[(2 * i + 1) % kChunks][j]));
+                        }
+                        store_row32<kBf16Out>(args.out, row, args.N, col, v);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    griddep_launch_dependents();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, kTmemCols);
     }
 }
 
-cudaError_t launch_mx_gemm(const MxGemmArgs& a, bool bf16_out, int num_sms, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>((a.R + kM - 1) / kM + a.n), static_cast<unsigned>((a.N + kN - 1) / kN));
-    if (a.b2_codes) {
-        if (bf16_out)
-            mx_gemm_simt_kernel<true, true><<<grid, kThreads, 0, st>>>(a);
-        else
-            mx_gemm_simt_kernel<true, false><<<grid, kThreads, 0, st>>>(a);
-    } else {
-        if (bf16_out)
-            mx_gemm_simt_kernel<false, true><<<grid, kThreads, 0, st>>>(a);
-        else
-            mx_gemm_simt_kernel<false, false><<<grid, kThreads, 0, st>>>(a);
-    }
-    return cudaGetLastError();
+int mx_gemm_tile_rows(int64_t R, int n) { return R <= 32 * static_cast<int64_t>(n) ? 32 : 128; }
+
+template <bool kPair, bool kBf16Out, int kBN, int kTM>
+static cudaError_t launch(const CUtensorMap* m, const MxGemmArgs& a, int num_sms, cudaStream_t st) {
+    constexpr int smem = smem_bytes<kBN, kTM>();
+    static_assert(smem <= 232448, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<kPair, kBf16Out, kBN, kTM>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t n_tiles = (a.N + (kPair ? 128 : kBN) - 1) / (kPair ? 128 : kBN);
+    int64_t g = ((a.R + kTM - 1) / kTM + a.n) * n_tiles;
+    if (g > num_sms) g = num_sms;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.a_scales) | reinterpret_cast<uintptr_t>(a.b_scales) |
+                         reinterpret_cast<uintptr_t>(a.b2_scales) | static_cast<uintptr_t>(a.K / 32);
+    const int how = at % 16 == 0 ? 4 : (at % 4 == 0 ? 2 : 1);
+    return launch_k(mx_gemm_kernel<kPair, kBf16Out, kBN, kTM>, dim3(static_cast<unsigned>(g)), dim3(kThreads), smem,
+                    st, m[0], m[1], m[2], a, how);
+}
+
+template <bool kPair, bool kBf16Out, int kBN>
+static cudaError_t launch_rows(const CUtensorMap* m, const MxGemmArgs& a, int num_sms, cudaStream_t st) {
+    return mx_gemm_tile_rows(a.R, a.n) == 32 ? launch<kPair, kBf16Out, kBN, 32>(m, a, num_sms, st)
+                                             : launch<kPair, kBf16Out, kBN, 128>(m, a, num_sms, st);
+}
+
+cudaError_t launch_mx_gemm(const CUtensorMap* m, const MxGemmArgs& a, bool bf16_out, int num_sms, cudaStream_t st) {
+    if (a.b2_codes)
+        return bf16_out ? launch_rows<true, true, 256>(m, a, num_sms, st)
+                        : launch_rows<true, false, 256>(m, a, num_sms, st);
+    // 256-column tiles halve the reads of A; 128-column ones are taken when the
+    // wide ones would leave SMs without a tile
+    const int64_t tm = mx_gemm_tile_rows(a.R, a.n);
+    const bool wide = ((a.R + tm - 1) / tm) * ((a.N + 255) / 256) >= num_sms;
+    if (wide)
+        return bf16_out ? launch_rows<false, true, 256>(m, a, num_sms, st)
+                        : launch_rows<false, false, 256>(m, a, num_sms, st);
+    return bf16_out ? launch_rows<false, true, 128>(m, a, num_sms, st)
+                    : launch_rows<false, false, 128>(m, a, num_sms, st);
 }
 
 }  // namespace moe

@@ -45,6 +45,9 @@ moe_status open_handle(moe_handle* h, HandleView* v);
 // outwards, strides of the axes after the first in bytes.
 bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                  const uint32_t* box);
+// The same for bytes.
+bool encode_bytes(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                  const uint32_t* box);
 moe_status failed(moe_status s, const char* fmt, ...);  // sets moe_last_error()
 moe_status done();
 

@@ -427,6 +427,9 @@ struct MxGemmArgs {
     void* out;
     int* status;
 };
-cudaError_t launch_mx_gemm(const MxGemmArgs& a, bool bf16_out, int num_sms, cudaStream_t st);
+// maps: A codes [R][K/2] in boxes of 128 bytes x mx_gemm_tile_rows rows, W and
+// the pair's codes [n][N][K/2] in boxes of 128 bytes x 128 rows.
+int mx_gemm_tile_rows(int64_t R, int n);
+cudaError_t launch_mx_gemm(const CUtensorMap* maps, const MxGemmArgs& a, bool bf16_out, int num_sms, cudaStream_t st);
 
 }  // namespace moe

@@ -339,8 +339,8 @@ moe_status check_device(moe_handle* h) {
 }  // namespace
 
 namespace moe_api_detail {
-bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-                 const uint32_t* box) {
+static bool encode(CUtensorMapDataType type, CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides, const uint32_t* box) {
     EncodeTiledFn f = encode_fn();
     if (!f) return false;
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
@@ -351,9 +351,17 @@ bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dim
         b[i] = box[i];
         if (i + 1 < rank) s[i] = strides[i];
     }
-    return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, es,
+    return f(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                 const uint32_t* box) {
+    return encode(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, m, base, rank, dims, strides, box);
+}
+bool encode_bytes(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                  const uint32_t* box) {
+    return encode(CU_TENSOR_MAP_DATA_TYPE_UINT8, m, base, rank, dims, strides, box);
 }
 
 moe_status open_handle(moe_handle* h, HandleView* v) {
