@@ -463,7 +463,8 @@ def _call_stream(s):
     already found on the current CUDA device."""
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the public call's time
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     return _stream(s)
 
 
@@ -488,8 +489,8 @@ def quantize_mxfp4(x, values: bool = False, stream=None):
     _take(where, "x", x, x.dtype, x.shape)
     cols, lead = x.shape[-1], x.shape[:-1]
     with _on(stream):
-        codes = torch.empty((*lead, cols // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((*lead, cols // 32), dtype=torch.uint8, device=x.device)
+        codes = x.new_empty((*lead, cols // 2), dtype=torch.uint8)
+        scales = x.new_empty((*lead, cols // 32), dtype=torch.uint8)
         v = torch.empty_like(x) if values else None
     moe_quantize_mxfp4(x.numel() // cols, cols, x, dt, codes, scales, v, _call_stream(stream))
     return (codes, scales, v) if values else (codes, scales)
@@ -508,9 +509,9 @@ def quantize_weights_mxfp4(w, values: bool = False, stream=None):
     _take(where, "w", w, w.dtype, w.shape)
     n, rows, cols = w.shape
     with _on(stream):
-        codes = torch.empty(n, cols, rows // 2, dtype=torch.uint8, device=w.device)
-        scales = torch.empty(n, cols, rows // 32, dtype=torch.uint8, device=w.device)
-        v = torch.empty(n, cols, rows, dtype=w.dtype, device=w.device) if values else None
+        codes = w.new_empty((n, cols, rows // 2), dtype=torch.uint8)
+        scales = w.new_empty((n, cols, rows // 32), dtype=torch.uint8)
+        v = w.new_empty((n, cols, rows)) if values else None
     moe_quantize_weights_mxfp4(n, rows, cols, w, dt, codes, scales, v, _call_stream(stream))
     return (codes, scales, v) if values else (codes, scales)
 
@@ -678,7 +679,7 @@ class MoELayer:
         with _on(stream):
             if y is None:
                 y = torch.empty_like(x)
-            gate = torch.empty(R, self.ffn, dtype=x.dtype, device=x.device) if keep else None
+            gate = x.new_empty((R, self.ffn)) if keep else None
             up = torch.empty_like(gate) if keep else None
         _take(where, "y", y, x.dtype, x.shape)
         moe_ffn_forward(self.h, R, offsets, x, w1, w3, w2, gate, up, y, _call_stream(stream))
@@ -727,7 +728,7 @@ class MoELayer:
         dt = self._torch_dtype()
         if out is None:
             with _on(stream):
-                out = torch.empty(R, N, dtype=dt, device=a[0].device)
+                out = a[0].new_empty((R, N), dtype=dt)
         _take(where, "out", out, dt, (R, N))
         p = pair if pair is not None else (None, None)
         moe_matmul_mxfp4(self.h, R, N, K, offsets, *a[:2], *w[:2], *p[:2], out, _call_stream(stream))

@@ -80,4 +80,54 @@ __device__ __forceinline__ int plan_expert(const SegmentPlan& p, int n, int b) {
     return lo;
 }
 
+// A warp's exchange block: 32 rows of 64 bytes in shared memory, the four
+// 16-byte pieces of row r at (piece ^ (r / 2 % 4)), free of bank conflicts both
+// by rows (a lane its row) and across them (four lanes a row).  The epilogues
+// hold one accumulator row per lane; written straight from registers, every
+// 16-byte store of a warp touches 32 lines of memory, half a sector each.
+// Through the block a store covers 8 rows of 64 contiguous bytes.
+constexpr int kExchangeBytes = 32 * 64;
+
+__device__ __forceinline__ uint4* exchange_at(uint8_t* block, int row, int piece) {
+    return reinterpret_cast<uint4*>(block + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+}
+
+// w: this lane's row, 16 words.  Row r < valid goes to out + r * ld_bytes
+// (16-byte aligned).  Every lane of the warp calls this.
+__device__ __forceinline__ void exchange_store(uint8_t* block, const uint32_t* w, int lane, int valid,
+                                               void* out, int64_t ld_bytes) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *exchange_at(block, lane, q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = j * 8 + (lane >> 2), q = lane & 3;
+        if (r < valid)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + r * ld_bytes + q * 16) = *exchange_at(block, r, q);
+    }
+    __syncwarp();
+}
+
+// The two halves of a load: fetch (in flight until its registers are used) and
+// the turn to one row per lane.  Rows past `valid` read zeros.
+__device__ __forceinline__ void exchange_fetch(uint4 (&v)[4], int lane, int valid, const void* src, int64_t ld_bytes) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = j * 8 + (lane >> 2), q = lane & 3;
+        v[j] = r < valid ? *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(src) + r * ld_bytes + q * 16)
+                         : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+__device__ __forceinline__ void exchange_turn(uint8_t* block, const uint4 (&v)[4], int lane, uint32_t (&w)[16]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *exchange_at(block, j * 8 + (lane >> 2), lane & 3) = v[j];
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint4 u = *exchange_at(block, lane, q);
+        w[4 * q] = u.x, w[4 * q + 1] = u.y, w[4 * q + 2] = u.z, w[4 * q + 3] = u.w;
+    }
+    __syncwarp();
+}
+
 }  // namespace moe

@@ -4,6 +4,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "../../include/moe.h"
 #include "handle.h"
 #include "kernels.h"
@@ -114,11 +116,11 @@ moe::FfnArgs ffn_args(const HandleView& v, int64_t R, const int32_t* offsets) {
 
 using moe_api_detail::encode_bf16;
 
-// Row operand [rows][cols]: 128 rows x 64 columns per copy.
-bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int cols) {
+// Row operand [rows][cols]: box_rows rows x 64 columns per copy.
+bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int cols, int box_rows) {
     const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
     const uint64_t strides[1] = {static_cast<uint64_t>(cols) * 2};
-    const uint32_t box[2] = {64, 128};
+    const uint32_t box[2] = {64, static_cast<uint32_t>(box_rows)};
     return encode_bf16(m, p, 2, dims, strides, box);
 }
 
@@ -152,19 +154,21 @@ moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t 
     if (v.bf16) {
         CUtensorMap m[4] = {};
         const int n = v.n, d = v.d, F = v.F;
+        const int few = moe::ffn_few_rows(op, a), box = few ? few : 128;
         bool ok = true;
         if (op == moe::kFfnUp)
-            ok = map_rows(&m[0], a.x, a.R, d) && map_weights_across(&m[2], a.w1, n, d, F) &&
+            ok = map_rows(&m[0], a.x, a.R, d, box) && map_weights_across(&m[2], a.w1, n, d, F) &&
                  map_weights_across(&m[3], a.w3, n, d, F);
         else if (op == moe::kFfnDown)
-            ok = map_rows(&m[0], a.h, a.R, F) && map_weights_across(&m[2], a.w2, n, F, d);
+            ok = map_rows(&m[0], a.h, a.R, F, box) && map_weights_across(&m[2], a.w2, n, F, d);
         else if (op == moe::kFfnGrad)
-            ok = map_rows(&m[0], a.dy, a.R, d) && map_weights(&m[2], a.w2, n, F, d);
+            ok = map_rows(&m[0], a.dy, a.R, d, box) && map_weights(&m[2], a.w2, n, F, d);
         else if (op == moe::kFfnDx)
-            ok = map_rows(&m[0], a.da, a.R, F) && map_rows(&m[1], a.db, a.R, F) &&
+            ok = map_rows(&m[0], a.da, a.R, F, box) && map_rows(&m[1], a.db, a.R, F, box) &&
                  map_weights(&m[2], a.w1, n, d, F) && map_weights(&m[3], a.w3, n, d, F);
         if (!ok) return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%s)", what);
-        e = moe::launch_ffn_tc(op, m, a, v.ffn->maps, v.num_sms, st);
+        e = few ? moe::launch_ffn_few(op, few, m, a, v.num_sms, st)
+                : moe::launch_ffn_tc(op, m, a, v.ffn->maps, v.num_sms, st);
     } else {
         e = moe::launch_ffn_simt(op, a, st);
     }
@@ -305,13 +309,22 @@ moe_status moe_ffn_backward(moe_handle* h, int64_t R, const int32_t* offsets, co
 }
 
 namespace {
+// SM count of the current device; what a device is never changes, so it is
+// asked for once per device.
 moe_status device_of_call(int* sms) {
-    int dev = 0, major = 0;
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices];
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_failed(e, "cudaGetDevice");
+    if (dev < kDevices && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return MOE_OK;
+    int major = 0, minor = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-    cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-    if (major != 10) return failed(MOE_ERR_UNSUPPORTED, "device %d is not sm_100", dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_failed(e, "cudaDeviceGetAttribute");
+    if (major != 10 || minor != 0) return failed(MOE_ERR_UNSUPPORTED, "device %d is not sm_100", dev);
+    if (dev < kDevices) known[dev].store(*sms, std::memory_order_relaxed);
     return MOE_OK;
 }
 }  // namespace

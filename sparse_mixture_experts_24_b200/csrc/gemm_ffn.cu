@@ -20,7 +20,7 @@
 //   warp 1     of the leader: tcgen05.mma.cta_group::2 (M 256, N 256, K 16);
 //   warps 2-9  epilogue, two per 32 accumulator rows, each on half the columns:
 //              the block's elementwise part on the fp32 accumulators, bf16
-//              rows.  Two accumulators (512 TMEM columns): a tile's epilogue
+//              rows through the warp's exchange block (ffn.cuh).  Two accumulators (512 TMEM columns): a tile's epilogue
 //              runs under the next tile's products.
 // kFfnDx adds both of its products in one accumulator: K simply runs over da
 // with w1 and then db with w3.  kFfnDw does all three weight gradients in one
@@ -57,7 +57,8 @@ struct __align__(16) Tail {
     uint32_t tmem_base;
     SegmentPlan plan;
 };
-constexpr int kSmemBytes = kStages * kStageBytes + (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128 + 1024;
+constexpr int kTailBytes = (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128;
+constexpr int kSmemBytes = kStages * kStageBytes + kTailBytes + kEpiWarps * kExchangeBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
 
 struct Tile {
@@ -133,19 +134,10 @@ __device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
                  : "memory");
 }
 
-// 32 columns of one row, as 16 words, to or from 64 contiguous bytes.
-__device__ __forceinline__ void store_words(void* base, int64_t at, const uint32_t (&w)[16]) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at);
+// 32 accumulators as 16 words of bf16 pairs.
+__device__ __forceinline__ void pack32(const uint32_t (&v)[32], uint32_t (&w)[16]) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-}
-__device__ __forceinline__ void load_words(const void* base, int64_t at, uint32_t (&w)[16]) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const uint4 v = src[q];
-        w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
-    }
+    for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
 }
 
 }  // namespace ffn_tc
@@ -328,93 +320,99 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t hand_back[2] = {mapa_shared(smem_u32(&tail->accum_empty[0]), 0),
                                        mapa_shared(smem_u32(&tail->accum_empty[1]), 0)};
         const FfnArgs& f = args.f;
+        uint8_t* block = smem + kStages * kStageBytes + kTailBytes + (warp - 2) * kExchangeBytes;
         int local = 0;
         for (int t = cid; t < total; t += ncl, ++local) {
             const Tile ti = tile_at<kOp>(t, plan, args);
             const int buf = local & 1;
             const uint32_t bph = static_cast<uint32_t>(local >> 1) & 1u;
+            uint4 gate_next[4], up_next[4];
+            if (kOp == kFfnGrad) {
+                const int r0 = 128 * static_cast<int>(rank) + 32 * quad;
+                const int col = ti.n_tile * kBN + half * 128;
+                const int64_t o = ((static_cast<int64_t>(ti.row0) + r0) * args.F + col) * 2;
+                const int valid = col < args.F ? ti.rows - r0 : 0;
+                exchange_fetch(gate_next, lane, valid, static_cast<const uint8_t*>(f.gate) + o, args.F * 2LL);
+                exchange_fetch(up_next, lane, valid, static_cast<const uint8_t*>(f.up) + o, args.F * 2LL);
+            }
             if (!mbar_wait(smem_u32(&tail->accum_full[buf]), bph, status, kStatusTimeoutAccum)) break;
             tc_fence_after();
             const uint32_t tbase =
                 tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(buf * kBN);
-            const int r = 128 * static_cast<int>(rank) + 32 * quad + lane;  // this thread's row of the tile
-            const bool row_ok = r < ti.rows;
-            const int64_t row = static_cast<int64_t>(ti.row0) + r;
-            if (kOp == kFfnUp) {
+            const int r0 = 128 * static_cast<int>(rank) + 32 * quad;  // this warp's 32 rows of the tile
+            const int valid = min(32, ti.rows - r0);                 // warp-uniform, like every column test
+            const int64_t row = static_cast<int64_t>(ti.row0) + r0;
+            if (valid <= 0) {
+                // nothing of this warp's to store
+            } else if (kOp == kFfnUp) {
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
                     const int at = half * 64 + c * 32;  // hidden columns of the tile
-                    uint32_t a[32], b[32];
+                    const int col = ti.n_tile * 128 + at;
+                    if (col >= args.F) break;
+                    uint32_t a[32], b[32], w[16];
                     tmem_ld_32x32b_x32(tbase + at, a);
                     tmem_ld_32x32b_x32(tbase + 128 + at, b);
                     tmem_wait_ld();
-                    const int col = ti.n_tile * 128 + at;
-                    if (row_ok && col < args.F) {
-                        const int64_t o = row * args.F + col;
-                        uint32_t w[16];
-                        if (f.gate) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                w[j] = pack_bf16x2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1]));
-                            store_words(f.gate, o, w);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                w[j] = pack_bf16x2(__uint_as_float(b[2 * j]), __uint_as_float(b[2 * j + 1]));
-                            store_words(f.up, o, w);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float h[2];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const float av = __uint_as_float(a[2 * j + i]);
-                                h[i] = av * sigmoid(av) * __uint_as_float(b[2 * j + i]);
-                            }
-                            w[j] = pack_bf16x2(h[0], h[1]);
-                        }
-                        store_words(f.h, o, w);
+                    const int64_t o = (row * args.F + col) * 2, ld = static_cast<int64_t>(args.F) * 2;
+                    if (f.gate) {
+                        pack32(a, w);
+                        exchange_store(block, w, lane, valid, static_cast<uint8_t*>(f.gate) + o, ld);
+                        pack32(b, w);
+                        exchange_store(block, w, lane, valid, static_cast<uint8_t*>(f.up) + o, ld);
                     }
-                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float h[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float av = __uint_as_float(a[2 * j + i]);
+                            h[i] = av * sigmoid(av) * __uint_as_float(b[2 * j + i]);
+                        }
+                        w[j] = pack_bf16x2(h[0], h[1]);
+                    }
+                    exchange_store(block, w, lane, valid, static_cast<uint8_t*>(f.h) + o, ld);
                 }
             } else if (kOp == kFfnGrad) {
+                // the first chunk of gate and up was fetched before the wait for the
+                // accumulator; chunk c + 1 is in flight while chunk c is computed
+                const int64_t ld = static_cast<int64_t>(args.F) * 2;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     const int at = half * 128 + c * 32;
                     const int col = ti.n_tile * kBN + at;
-                    const bool in = row_ok && col < args.F;
-                    const int64_t o = row * args.F + col;
+                    if (col >= args.F) break;
+                    const int64_t o = (row * args.F + col) * 2;
                     uint32_t ga[16], gb[16], dh[32];
-                    if (in) {
-                        load_words(f.gate, o, ga);
-                        load_words(f.up, o, gb);
-                    }
-                    __syncwarp();
                     tmem_ld_32x32b_x32(tbase + at, dh);
-                    tmem_wait_ld();
-                    if (in) {
-                        uint32_t da[16], db[16], hw[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float a[2], b[2], x[2], y[2], h[2];
-                            unpack_bf16x2(ga[j], a[0], a[1]);
-                            unpack_bf16x2(gb[j], b[0], b[1]);
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const float s = sigmoid(a[i]), g = __uint_as_float(dh[2 * j + i]);
-                                const float as = a[i] * s;
-                                h[i] = as * b[i];
-                                y[i] = g * as;
-                                x[i] = g * b[i] * (s + as * (1.f - s));
-                            }
-                            da[j] = pack_bf16x2(x[0], x[1]);
-                            db[j] = pack_bf16x2(y[0], y[1]);
-                            hw[j] = pack_bf16x2(h[0], h[1]);
-                        }
-                        store_words(f.da, o, da);
-                        store_words(f.db, o, db);
-                        store_words(f.h, o, hw);
+                    exchange_turn(block, gate_next, lane, ga);
+                    exchange_turn(block, up_next, lane, gb);
+                    if (c < 3 && col + 32 < args.F) {
+                        exchange_fetch(gate_next, lane, valid, static_cast<const uint8_t*>(f.gate) + o + 64, ld);
+                        exchange_fetch(up_next, lane, valid, static_cast<const uint8_t*>(f.up) + o + 64, ld);
                     }
-                    __syncwarp();
+                    tmem_wait_ld();
+                    uint32_t hw[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float a[2], b[2], x[2], y[2], h[2];
+                        unpack_bf16x2(ga[j], a[0], a[1]);
+                        unpack_bf16x2(gb[j], b[0], b[1]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float s = sigmoid(a[i]), g = __uint_as_float(dh[2 * j + i]);
+                            const float as = a[i] * s;
+                            h[i] = as * b[i];
+                            y[i] = g * as;
+                            x[i] = g * b[i] * (s + as * (1.f - s));
+                        }
+                        ga[j] = pack_bf16x2(x[0], x[1]);
+                        gb[j] = pack_bf16x2(y[0], y[1]);
+                        hw[j] = pack_bf16x2(h[0], h[1]);
+                    }
+                    exchange_store(block, ga, lane, valid, static_cast<uint8_t*>(f.da) + o, ld);
+                    exchange_store(block, gb, lane, valid, static_cast<uint8_t*>(f.db) + o, ld);
+                    exchange_store(block, hw, lane, valid, static_cast<uint8_t*>(f.h) + o, ld);
                 }
             } else {
                 // Down, Dx: columns of y or dx.  Dw: half 0 of a dw1 | dw3 tile is
@@ -426,19 +424,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     (kOp == kFfnDw ? static_cast<int64_t>(ti.e) * args.d * args.F : 0) + row * cols + col0;
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
+                    if (col0 + c * 32 >= cols) break;
                     uint32_t v[32], w[16];
                     if (ti.steps > 0) {
                         tmem_ld_32x32b_x32(tbase + half * 128 + c * 32, v);
                         tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                        pack32(v, w);
                     } else {  // an expert without rows
 #pragma unroll
                         for (int j = 0; j < 16; ++j) w[j] = 0u;
                     }
-                    if (row_ok && col0 + c * 32 < cols) store_words(out, base + c * 32, w);
-                    __syncwarp();
+                    exchange_store(block, w, lane, valid, static_cast<uint16_t*>(out) + base + c * 32,
+                                   static_cast<int64_t>(cols) * 2);
                 }
             }
             tc_fence_before();

@@ -1,0 +1,340 @@
+// gemm_ffn_few.cu -- the row products of the gated feed-forward block
+// (gemm_ffn.cu: kFfnUp, kFfnDown, kFfnGrad, kFfnDx) in bf16 for few rows per
+// expert, where the call is bound by reading the weights once.
+//
+// The product is turned over: 128 weight columns are the MMA's M and kT rows of
+// the batch its N, so a tile needs no padding to 256 rows and there are enough
+// tiles to keep all SMs loading; where there are not (one dense expert's
+// 14,336 x 4,096 output projection has 32), the reduction is split over a
+// cluster of up to 8 CTAs, whose partial sums meet in distributed shared
+// memory, added in rank order.  Both operands keep their layouts: the weights
+// are M-major for kFfnUp and kFfnDown (their rows are the reduction) and
+// K-major for the other two, the rows are K-major.
+//
+// 192 threads, one CTA per SM (the ring takes its shared memory):
+//   warp 0     TMA, 64 of K per step: 128 weight columns (kFfnUp: of both
+//              matrices) and kT rows;
+//   warp 1     tcgen05.mma M 128, N kT, K 16 (kFfnUp: two accumulators);
+//   warps 2-5  epilogue: a thread holds one weight column of every row.
+// The weights do not depend on the kernel before: their copies for the whole
+// ring start before the programmatic-launch wait, under its last tiles.
+// Every wait is bounded (common.cuh).
+#include <algorithm>
+
+#include "ffn.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace ffn_few {
+
+constexpr int kBM = 128, kBK = 64;
+constexpr int kWBytes = kBM * kBK * 2;   // 16 KB: 128 columns of one matrix
+constexpr int kChunk = 64 * kBK * 2;     // 8 KB: 64 columns, M-major
+constexpr int kThreads = 192;
+constexpr int kMaxStages = 8;
+constexpr int kRingBytes = 216 * 1024;
+
+template <int kOp, int kT>
+struct Cfg {
+    static constexpr int kMats = kOp == kFfnUp ? 2 : 1;
+    static constexpr int kStageBytes = kMats * kWBytes + kT * kBK * 2;
+    static constexpr int kStages = kRingBytes / kStageBytes < kMaxStages ? kRingBytes / kStageBytes : kMaxStages;
+    static constexpr int kTmemCols = kMats * kT < 32 ? 32 : kMats * kT;
+    // the ring holds the partial sums of a split reduction afterwards
+    static_assert(kMats * kT * kBM * 4 <= kStages * kStageBytes, "partial sums");
+};
+
+struct __align__(16) Tail {
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    uint64_t accum_full;
+    uint32_t tmem_base;
+    SegmentPlan plan;
+};
+constexpr int kTailBytes = (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128;
+
+template <int kOp, int kT>
+constexpr int smem_bytes() {
+    return Cfg<kOp, kT>::kStages * Cfg<kOp, kT>::kStageBytes + kTailBytes + 1024;
+}
+
+__device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.f, 1.f + __expf(-a)); }
+
+__device__ __forceinline__ float load_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void put(void* base, int64_t at, float v) {
+    static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(v);
+}
+__device__ __forceinline__ float get(const void* base, int64_t at) {
+    return bf16_bits_to_float(static_cast<const uint16_t*>(base)[at]);
+}
+
+// One output: weight column col, row `row` of the batch, accumulators v (and u,
+// kFfnUp).
+template <int kOp>
+__device__ __forceinline__ void finish(const FfnArgs& f, int64_t row, int col, float v, float u) {
+    if (kOp == kFfnUp) {
+        const int64_t at = row * f.F + col;
+        if (f.gate) {
+            put(f.gate, at, v);
+            put(f.up, at, u);
+        }
+        put(f.h, at, v * sigmoid(v) * u);
+    } else if (kOp == kFfnGrad) {
+        const int64_t at = row * f.F + col;
+        const float a = get(f.gate, at), b = get(f.up, at), s = sigmoid(a), as = a * s;
+        put(f.h, at, as * b);
+        put(f.db, at, v * as);
+        put(f.da, at, v * b * (s + as * (1.f - s)));
+    } else {
+        put(kOp == kFfnDown ? f.y : f.dx, row * f.d + col, v);
+    }
+}
+
+}  // namespace ffn_few
+
+using namespace ffn_few;
+
+template <int kOp, int kT>
+__global__ void __launch_bounds__(ffn_few::kThreads, 1)
+    ffn_few_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
+                   const __grid_constant__ CUtensorMap tm_b0, const __grid_constant__ CUtensorMap tm_b1,
+                   const FfnArgs f, const int steps, const int splits) {
+    using C = Cfg<kOp, kT>;
+    constexpr bool kWMn = kOp == kFfnUp || kOp == kFfnDown;  // the weights are M-major
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    ffn_few::Tail* tail = reinterpret_cast<ffn_few::Tail*>(smem + C::kStages * C::kStageBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    load_plan(tail->plan, f.offsets, f.n, f.R, kT, f.status);
+    const SegmentPlan& plan = tail->plan;
+    griddep_launch_dependents();
+    // x: weight column tile and, fastest, the split of its reduction; y: row block
+    if (static_cast<int>(blockIdx.y) >= plan.blk[f.n]) {
+        griddep_wait();
+        return;  // the whole cluster: its CTAs share blockIdx.y
+    }
+    const int rank = static_cast<int>(blockIdx.x) % splits, tile = static_cast<int>(blockIdx.x) / splits;
+    const int e = plan_expert(plan, f.n, blockIdx.y);
+    const int row0 = plan.off[e] + (static_cast<int>(blockIdx.y) - plan.blk[e]) * kT;
+    const int rows = min(kT, plan.off[e + 1] - row0);
+    const int col0 = tile * kBM;
+    const int k0 = static_cast<int>(static_cast<int64_t>(steps) * rank / splits);
+    const int k1 = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / splits);
+    int* status = f.status;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(smem_u32(&tail->full[s]), 1);
+            mbar_init(smem_u32(&tail->empty[s]), 1);
+        }
+        mbar_init(smem_u32(&tail->accum_full), 1);
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&tail->tmem_base), C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = tail->tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA ----------------
+            auto weights = [&](int kb, int stage) {
+                const uint32_t fb = smem_u32(&tail->full[stage]);
+                mbar_arrive_expect_tx(fb, C::kStageBytes);
+                const uint32_t dst = smem_u32(smem + stage * C::kStageBytes);
+                int k = kb * kBK;
+                if (kOp == kFfnUp) {
+                    tma_load_4d(dst, &tm_b0, fb, 0, k, tile * 2, e);
+                    tma_load_4d(dst + kWBytes, &tm_b1, fb, 0, k, tile * 2, e);
+                } else if (kOp == kFfnDown) {
+                    tma_load_4d(dst, &tm_b0, fb, 0, k, tile * 2, e);
+                } else if (kOp == kFfnGrad) {
+                    tma_load_3d(dst, &tm_b0, fb, k, col0, e);
+                } else {
+                    const bool second = k >= f.F;
+                    tma_load_3d(dst, second ? &tm_b1 : &tm_b0, fb, second ? k - f.F : k, col0, e);
+                }
+            };
+            auto batch = [&](int kb, int stage) {
+                const uint32_t fb = smem_u32(&tail->full[stage]);
+                const uint32_t dst = smem_u32(smem + stage * C::kStageBytes) + C::kMats * kWBytes;
+                const int k = kb * kBK;
+                const bool second = kOp == kFfnDx && k >= f.F;
+                tma_load_2d(dst, second ? &tm_a1 : &tm_a0, fb, second ? k - f.F : k, row0);
+            };
+            const int ahead = min(C::kStages, k1 - k0);
+            for (int i = 0; i < ahead; ++i) weights(k0 + i, i);
+            griddep_wait();
+            for (int i = 0; i < ahead; ++i) batch(k0 + i, i);
+            bool ok = true;
+            for (int i = ahead; i < k1 - k0; ++i) {
+                const int stage = i % C::kStages;
+                const uint32_t use = static_cast<uint32_t>(i / C::kStages);
+                if (!mbar_wait(smem_u32(&tail->empty[stage]), (use & 1u) ^ 1u, status, kStatusTimeoutEmpty)) {
+                    ok = false;
+                    break;
+                }
+                weights(k0 + i, stage);
+                batch(k0 + i, stage);
+            }
+            if (!ok)  // give every armed copy its time to land before the CTA leaves
+                for (int s = 0; s < C::kStages; ++s)
+                    mbar_wait(smem_u32(&tail->full[s]), 0, status, kStatusTimeoutDrain);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- MMA ----------------
+            constexpr uint32_t idesc = make_idesc_bf16(kBM, kT, kWMn ? 1 : 0, 0);
+            bool ok = true;
+            for (int i = 0; i < k1 - k0; ++i) {
+                const int stage = i % C::kStages;
+                const uint32_t use = static_cast<uint32_t>(i / C::kStages);
+                if (!mbar_wait(smem_u32(&tail->full[stage]), use & 1u, status, kStatusTimeoutFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t base = smem_u32(smem + stage * C::kStageBytes);
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk) {
+                    const uint64_t bd = make_smem_desc(base + C::kMats * kWBytes + kk * 32, 16, 1024, 2);
+#pragma unroll
+                    for (int m = 0; m < C::kMats; ++m) {
+                        const uint32_t a = base + m * kWBytes;
+                        const uint64_t ad = kWMn ? make_smem_desc(a + kk * 2048, kChunk, 1024, 2)
+                                                 : make_smem_desc(a + kk * 32, 16, 1024, 2);
+                        tc_mma_f16(tmem_base + static_cast<uint32_t>(m * kT), ad, bd, idesc, (i | kk) != 0 ? 1u : 0u);
+                    }
+                }
+                tc_commit(smem_u32(&tail->empty[stage]));
+            }
+            (void)ok;
+            tc_commit(smem_u32(&tail->accum_full));
+            mbar_wait(smem_u32(&tail->accum_full), 0, status, kStatusTimeoutDrain);
+        }
+    } else {
+        // ---------------- accumulators ----------------
+        const int quad = warp & 3;  // TMEM lanes 32 * quad .. + 31
+        const int c = quad * 32 + lane;
+        const int cols = kOp == kFfnUp || kOp == kFfnGrad ? f.F : f.d;
+        const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+        const bool done = mbar_wait(smem_u32(&tail->accum_full), 0, status, kStatusTimeoutAccum);
+        __syncwarp();
+        tc_fence_after();
+        float* part = reinterpret_cast<float*>(smem);  // [matrix][row][128 columns]
+        if (done) {
+#pragma unroll 1
+            for (int t0 = 0; t0 < rows; t0 += 16) {
+                uint32_t v[16], u[16];
+                tmem_ld_32x32b_x16(tbase + t0, v);
+                if (kOp == kFfnUp) tmem_ld_32x32b_x16(tbase + kT + t0, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float vf = __uint_as_float(v[i]), uf = kOp == kFfnUp ? __uint_as_float(u[i]) : 0.f;
+                    if (splits > 1) {
+                        part[(t0 + i) * kBM + c] = vf;
+                        if (kOp == kFfnUp) part[(kT + t0 + i) * kBM + c] = uf;
+                    } else if (t0 + i < rows && col0 + c < cols) {
+                        finish<kOp>(f, static_cast<int64_t>(row0) + t0 + i, col0 + c, vf, uf);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    __syncwarp();
+    if (splits > 1) {
+        // every CTA of the cluster finishes its share of the rows
+        cluster_sync();
+        const int cols = kOp == kFfnUp || kOp == kFfnGrad ? f.F : f.d;
+        const uint32_t part = smem_u32(smem);
+        if (threadIdx.x < kBM && col0 + static_cast<int>(threadIdx.x) < cols) {
+            for (int t = rank; t < rows; t += splits) {
+                float v = 0.f, u = 0.f;
+                for (int q = 0; q < splits; ++q) {
+                    v += load_cluster(mapa_shared(part + (t * kBM + threadIdx.x) * 4, q));
+                    if (kOp == kFfnUp) u += load_cluster(mapa_shared(part + ((kT + t) * kBM + threadIdx.x) * 4, q));
+                }
+                finish<kOp>(f, static_cast<int64_t>(row0) + t, col0 + static_cast<int>(threadIdx.x), v, u);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // the partial sums stay until every CTA has read them
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::kTmemCols);
+    }
+}
+
+template <int kOp, int kT>
+static cudaError_t launch_few(const CUtensorMap* m, const FfnArgs& f, int num_sms, cudaStream_t st) {
+    constexpr int smem = smem_bytes<kOp, kT>();
+    static_assert(smem <= 232448, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(ffn_few_kernel<kOp, kT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int cols = kOp == kFfnUp || kOp == kFfnGrad ? f.F : f.d;
+    const int K = kOp == kFfnUp || kOp == kFfnGrad ? f.d : (kOp == kFfnDown ? f.F : 2 * f.F);
+    const int64_t tiles = (cols + kBM - 1) / kBM;
+    const int64_t blocks = (f.R + kT - 1) / kT + f.n;  // at most
+    // row blocks that are likely there: one per expert that has rows
+    const int64_t likely = std::max<int64_t>((f.R + kT - 1) / kT, std::min<int64_t>(f.n, f.R));
+    int splits = 1;
+    while (splits < 8 && tiles * likely * splits * 2 <= num_sms && K / kBK >= 8 * splits) splits *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(ffn_few::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = (g_chain_started && pdl_enabled()) ? 2 : 1;
+    g_chain_started = true;
+    return cudaLaunchKernelEx(&cfg, ffn_few_kernel<kOp, kT>, m[0], m[1], m[2], m[3], f, K / kBK, splits);
+}
+
+template <int kT>
+static cudaError_t launch_few_op(int op, const CUtensorMap* m, const FfnArgs& f, int num_sms, cudaStream_t st) {
+    switch (op) {
+        case kFfnUp: return launch_few<kFfnUp, kT>(m, f, num_sms, st);
+        case kFfnDown: return launch_few<kFfnDown, kT>(m, f, num_sms, st);
+        case kFfnGrad: return launch_few<kFfnGrad, kT>(m, f, num_sms, st);
+        case kFfnDx: return launch_few<kFfnDx, kT>(m, f, num_sms, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+int ffn_few_rows(int op, const FfnArgs& f) {
+    if (op == kFfnDw) return 0;
+    if (f.R <= 32 * static_cast<int64_t>(f.n)) return 32;
+    if (f.R <= 96 * static_cast<int64_t>(f.n)) return 128;
+    return 0;
+}
+
+cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, int num_sms, cudaStream_t st) {
+    return rows == 32 ? launch_few_op<32>(op, maps, f, num_sms, st) : launch_few_op<128>(op, maps, f, num_sms, st);
+}
+
+}  // namespace moe

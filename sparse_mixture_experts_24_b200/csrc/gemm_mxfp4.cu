@@ -66,10 +66,11 @@ struct __align__(16) Tail {
     SegmentPlan plan;
 };
 
+constexpr int kTailBytes = (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128;
+
 template <int kBN, int kTM>
 constexpr int smem_bytes() {
-    return Cfg<kBN, kTM>::kStages * Cfg<kBN, kTM>::kStageBytes + (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128 +
-           1024;
+    return Cfg<kBN, kTM>::kStages * Cfg<kBN, kTM>::kStageBytes + kTailBytes + kEpiWarps * kExchangeBytes + 1024;
 }
 
 struct Tile {
@@ -141,34 +142,36 @@ __device__ __forceinline__ uint4 load_scales(const uint8_t* row, int g, int nb, 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Columns col .. col+31 of one row of out.
+// Columns col .. col+31 of 32 rows of out (a lane its row, `valid` of them).
+// Rows that are whole vectors go through the warp's exchange block, others
+// element by element.
 template <bool kBf16>
-__device__ __forceinline__ void store_row32(void* out, int64_t row, int N, int col, const uint32_t (&bits)[32]) {
-    auto v = [&](int j) { return __uint_as_float(bits[j]); };
-    const int64_t at = row * N + col;
+__device__ __forceinline__ void store_rows(uint8_t* block, void* out, int64_t row0, int valid, int lane, int N,
+                                           int col, const uint32_t (&v)[32]) {
     if (kBf16) {
-        uint16_t* o = static_cast<uint16_t*>(out) + at;
+        uint16_t* o = static_cast<uint16_t*>(out) + row0 * N + col;
         if (N % 8 == 0 && col + 32 <= N) {
+            uint32_t w[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                reinterpret_cast<uint4*>(o)[q] =
-                    make_uint4(pack_bf16x2(v(8 * q), v(8 * q + 1)), pack_bf16x2(v(8 * q + 2), v(8 * q + 3)),
-                               pack_bf16x2(v(8 * q + 4), v(8 * q + 5)), pack_bf16x2(v(8 * q + 6), v(8 * q + 7)));
-        } else {
+            for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+            exchange_store(block, w, lane, valid, o, static_cast<int64_t>(N) * 2);
+        } else if (lane < valid) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (col + j < N) o[j] = static_cast<uint16_t>(pack_bf16x2(v(j), 0.f));
+                if (col + j < N)
+                    o[static_cast<int64_t>(lane) * N + j] =
+                        static_cast<uint16_t>(pack_bf16x2(__uint_as_float(v[j]), 0.f));
         }
     } else {
-        float* o = static_cast<float*>(out) + at;
+        float* o = static_cast<float*>(out) + row0 * N + col;
         if (N % 4 == 0 && col + 32 <= N) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                reinterpret_cast<float4*>(o)[q] = make_float4(v(4 * q), v(4 * q + 1), v(4 * q + 2), v(4 * q + 3));
-        } else {
+            for (int h = 0; h < 2; ++h)
+                exchange_store(block, v + 16 * h, lane, valid, o + 16 * h, static_cast<int64_t>(N) * 4);
+        } else if (lane < valid) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (col + j < N) o[j] = v(j);
+                if (col + j < N) o[static_cast<int64_t>(lane) * N + j] = __uint_as_float(v[j]);
         }
     }
 }
@@ -384,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quad = warp & 3;         // TMEM lanes 32 * quad .. + 31
         const int half = (warp - 2) >> 2;  // half of the columns
         constexpr int kChunks = kBN / 64;  // 32-column chunks per warp
+        uint8_t* block = smem + C::kStages * C::kStageBytes + kTailBytes + (warp - 2) * kExchangeBytes;
         int local = 0;
         for (int t = first; t < total; t += stride, ++local) {
             const Tile ti = tile_at<kTM>(t, plan, args.n, n_tiles);
@@ -393,9 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t tbase =
                 tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(buf * kBN);
-            const bool any = quad * 32 < ti.rows;  // warp-uniform
-            const bool row_ok = quad * 32 + lane < ti.rows;
-            const int64_t row = static_cast<int64_t>(ti.row0) + quad * 32 + lane;
+            const int valid = min(32, ti.rows - quad * 32);  // warp-uniform
+            const bool any = valid > 0;
+            const int64_t row0 = static_cast<int64_t>(ti.row0) + quad * 32;
             uint32_t acc[kChunks][32];
             if (any) {
 #pragma unroll
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&tail->accum_empty[buf]));
-            if (row_ok) {
+            if (any) {
 #pragma unroll
                 for (int i = 0; i < (kPair ? kChunks / 2 : kChunks); ++i) {
                     const int col = kPair ? ti.n_tile * 128 + half * 64 + i * 32
@@ -422,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 v[j] = __float_as_uint(silu<kBf16Out>(__uint_as_float(v[j])) *
                                                        __uint_as_float(acc[(2 * i + 1) % kChunks][j]));
                         }
-                        store_row32<kBf16Out>(args.out, row, args.N, col, v);
+                        store_rows<kBf16Out>(block, args.out, row0, valid, lane, args.N, col, v);
                     }
                 }
             }

@@ -404,6 +404,11 @@ struct FfnTcArgs {
 };
 cudaError_t launch_ffn_maps(const CUtensorMap* maps5, const int32_t* offsets, int n, int64_t R, void* out,
                             int* status, cudaStream_t st);
+// The row ops for few rows per expert (gemm_ffn_few.cu): ffn_few_rows gives the
+// batch rows of its tiles (the box of the row operands' maps), or 0 where
+// launch_ffn_tc is to be taken.  The weights' maps are the same.
+int ffn_few_rows(int op, const FfnArgs& f);
+cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, int num_sms, cudaStream_t st);
 cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnArgs& f, const void* dw_maps, int num_sms,
                           cudaStream_t st);
 

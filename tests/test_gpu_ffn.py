@@ -44,6 +44,13 @@ SHAPES = [
     (8, [16, 15, 17, 0, 33, 32, 31, 2], 146, 1, 1, 192, 576),
     (2, [300, 513], 813, 0, 0, 512, 256),
     (33, [7, 0, 1] * 11, 88, 0, 0, 64, 128),
+    # few rows: reductions split over clusters of 2, 4 and 8, one and several row blocks
+    (1, None, 5, 0, 0, 1024, 1536),
+    (1, None, 2, 0, 0, 64, 4096),
+    (2, [40, 3], 43, 0, 2, 1024, 704),
+    (3, [90, 0, 131], 221, 4, 0, 576, 1088),
+    # more tiles than SMs: every CTA pair runs several, through both accumulators
+    (3, [700, 0, 1001], 1701, 0, 3, 1024, 2112),
 ]
 
 

@@ -100,6 +100,8 @@ PRODUCTS = [
     (2, [0, 31, 63], 63, 513, 1056),
     (9, [0, 1, 3, 6, 10, 15, 21, 28, 36, 45], 45, 256, 2048),
     (2, [0, 300, 300], 300, 1000, 768),
+    # more tiles than SMs, and scale rows that are not whole words
+    (4, [0, 500, 500, 777, 1201], 1201, 4104, 1184),
 ]
 
 
