@@ -170,7 +170,7 @@ moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t 
         e = few ? moe::launch_ffn_few(op, few, m, a, v.num_sms, st)
                 : moe::launch_ffn_tc(op, m, a, v.ffn->maps, v.num_sms, st);
     } else {
-        e = moe::launch_ffn_simt(op, a, st);
+        e = moe::launch_ffn_simt(op, a, v.num_sms, st);
     }
     if (e != cudaSuccess) return cuda_failed(e, what);
     *v.launches += 1;

@@ -15,6 +15,11 @@
 // so that the pairs a, b and da, db of one hidden column meet in one thread.
 // The reduction runs in chunks of 16 through two shared-memory buffers, the
 // next chunk's global loads in flight while the current one is multiplied.
+// One warp per scheduler issues a multiply-add every other cycle at best, and
+// small batches have fewer tiles than SMs: a row product is then split along
+// its reduction over a cluster of up to 8 blocks, whose partial sums meet in
+// distributed shared memory and are added in rank order.
+#include <algorithm>
 #include <cstddef>
 
 #include "ffn.cuh"
@@ -29,23 +34,41 @@ constexpr int kM = 64, kN = 128, kK = 16, kThreads = 128;
 __device__ __forceinline__ float4 load4(const void* p, int64_t i) {
     return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
 }
+// Two fp32 multiply-adds in one instruction, each rounded as fmaf: the loop is
+// bound by issue slots, and this halves them.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+
 __device__ __forceinline__ void store4(void* p, int64_t i, float a, float b, float c, float d) {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(a, b, c, d);
 }
 
-struct __align__(16) Smem {
+struct Tiles {
     float a[2][kK][kM + 4];  // rows of both arrays stay 16-byte aligned: they are read as float4
     float b[2][kK][kN + 4];
+};
+struct __align__(16) Smem {
+    union {
+        Tiles t;
+        float part[64][kThreads];  // a split reduction's accumulators: [value of the thread][thread]
+    };
     SegmentPlan plan;
 };
-static_assert((kM + 4) % 4 == 0 && (kN + 4) % 4 == 0 && offsetof(Smem, b) % 16 == 0, "float4 alignment");
+static_assert((kM + 4) % 4 == 0 && (kN + 4) % 4 == 0 && offsetof(Tiles, b) % 16 == 0, "float4 alignment");
 
 }  // namespace ffn_simt
 
 using namespace ffn_simt;
 
 template <int kOp>
-__global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
+__global__ void __launch_bounds__(kThreads, kOp == kFfnGrad || kOp == kFfnDx ? 4 : 3)
+    ffn_simt_kernel(const FfnArgs g, const int splits) {
     griddep_wait();
     __shared__ Smem sm;
     load_plan(sm.plan, g.offsets, g.n, g.R, kM, g.status);
@@ -70,9 +93,11 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
         col[1] = dw2 ? c * kN + 64 : c * 64;
         K = sm.plan.off[e + 1] - sm.plan.off[e];
     } else {
-        if (static_cast<int>(blockIdx.x) >= sm.plan.blk[g.n]) return;
-        e = plan_expert(sm.plan, g.n, blockIdx.x);
-        row0 = sm.plan.off[e] + (static_cast<int>(blockIdx.x) - sm.plan.blk[e]) * kM;
+        // x: row block and, fastest, the split of its reduction (one cluster)
+        const int b = static_cast<int>(blockIdx.x) / splits;
+        if (b >= sm.plan.blk[g.n]) return;
+        e = plan_expert(sm.plan, g.n, b);
+        row0 = sm.plan.off[e] + (b - sm.plan.blk[e]) * kM;
         rows = min(kM, sm.plan.off[e + 1] - row0);
         const int c = blockIdx.y;
         col[0] = kOp == kFfnUp ? c * 64 : c * kN;
@@ -145,13 +170,13 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
         for (int i = 0; i < 2; ++i) {
             const int p = tid + i * kThreads;
             if (kOp == kFfnDw) {
-                *reinterpret_cast<float4*>(&sm.a[buf][p >> 4][(p & 15) * 4]) = ra[i];
+                *reinterpret_cast<float4*>(&sm.t.a[buf][p >> 4][(p & 15) * 4]) = ra[i];
             } else {
                 const int r = p >> 2, k = (p & 3) * 4;
-                sm.a[buf][k][r] = ra[i].x;
-                sm.a[buf][k + 1][r] = ra[i].y;
-                sm.a[buf][k + 2][r] = ra[i].z;
-                sm.a[buf][k + 3][r] = ra[i].w;
+                sm.t.a[buf][k][r] = ra[i].x;
+                sm.t.a[buf][k + 1][r] = ra[i].y;
+                sm.t.a[buf][k + 2][r] = ra[i].z;
+                sm.t.a[buf][k + 3][r] = ra[i].w;
             }
         }
 #pragma unroll
@@ -159,52 +184,90 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
             const int p = tid + i * kThreads;
             if (kOp == kFfnGrad || kOp == kFfnDx) {
                 const int n = p >> 2, k = (p & 3) * 4;
-                sm.b[buf][k][n] = rb[i].x;
-                sm.b[buf][k + 1][n] = rb[i].y;
-                sm.b[buf][k + 2][n] = rb[i].z;
-                sm.b[buf][k + 3][n] = rb[i].w;
+                sm.t.b[buf][k][n] = rb[i].x;
+                sm.t.b[buf][k + 1][n] = rb[i].y;
+                sm.t.b[buf][k + 2][n] = rb[i].z;
+                sm.t.b[buf][k + 3][n] = rb[i].w;
             } else {
-                *reinterpret_cast<float4*>(&sm.b[buf][p >> 5][(p & 31) * 4]) = rb[i];
+                *reinterpret_cast<float4*>(&sm.t.b[buf][p >> 5][(p & 31) * 4]) = rb[i];
             }
         }
     };
 
-    float acc[8][8];
+    uint64_t acc2[8][4];  // two neighbouring columns each
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) acc2[i][j] = 0ull;
 
-    const int64_t chunks = (K + kK - 1) / kK;
+    const int rank = kOp == kFfnDw ? 0 : static_cast<int>(blockIdx.x) % splits;
+    const int64_t all = (K + kK - 1) / kK, c0 = kOp == kFfnDw ? 0 : all * rank / splits;
+    const int64_t chunks = kOp == kFfnDw ? all : all * (rank + 1) / splits - c0;
     if (chunks > 0) {
-        fetch(0);
+        fetch(c0 * kK);
         put(0);
     }
     __syncthreads();
     for (int64_t c = 0; c < chunks; ++c) {
         const int buf = static_cast<int>(c & 1);
-        if (c + 1 < chunks) fetch((c + 1) * kK);
+        if (c + 1 < chunks) fetch((c0 + c + 1) * kK);
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
-            const float4 a0 = *reinterpret_cast<const float4*>(&sm.a[buf][k][ty * 8]);
-            const float4 a1 = *reinterpret_cast<const float4*>(&sm.a[buf][k][ty * 8 + 4]);
-            const float4 b0 = *reinterpret_cast<const float4*>(&sm.b[buf][k][tx * 4]);
-            const float4 b1 = *reinterpret_cast<const float4*>(&sm.b[buf][k][64 + tx * 4]);
+            const float4 a0 = *reinterpret_cast<const float4*>(&sm.t.a[buf][k][ty * 8]);
+            const float4 a1 = *reinterpret_cast<const float4*>(&sm.t.a[buf][k][ty * 8 + 4]);
+            const float4 b0 = *reinterpret_cast<const float4*>(&sm.t.b[buf][k][tx * 4]);
+            const float4 b1 = *reinterpret_cast<const float4*>(&sm.t.b[buf][k][64 + tx * 4]);
             const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-            const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+            const uint64_t bv[4] = {pair2(b0.x, b0.y), pair2(b0.z, b0.w), pair2(b1.x, b1.y), pair2(b1.z, b1.w)};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t a2 = pair2(av[i], av[i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+                for (int j = 0; j < 4; ++j) fma2(acc2[i][j], a2, bv[j]);
+            }
         }
         if (c + 1 < chunks) put(buf ^ 1);
         __syncthreads();
     }
 
+    float acc[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[i][2 * j]), "=f"(acc[i][2 * j + 1]) : "l"(acc2[i][j]));
+    if (kOp != kFfnDw && splits > 1) {
+        // rank q finishes rows i = q, q + splits, ... of every thread's eight
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sm.part[i * 8 + j][tid] = acc[i][j];
+        cluster_sync();
+        const uint32_t mine = smem_u32(&sm.part[0][tid]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i % splits != rank) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float v = 0.f;
+                for (int q = 0; q < splits; ++q) {
+                    float u;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(u)
+                                 : "r"(mapa_shared(mine + (i * 8 + j) * kThreads * 4, q))
+                                 : "memory");
+                    v += u;
+                }
+                acc[i][j] = v;
+            }
+        }
+        cluster_sync();  // the partial sums stay until every block has read them
+    }
+
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = ty * 8 + i;
-        if (r >= rows) continue;
+        if (r >= rows || (kOp != kFfnDw && i % splits != rank)) continue;
         const int64_t row = static_cast<int64_t>(row0) + r;
         const float* v = acc[i];
         if (kOp == kFfnUp) {
@@ -250,21 +313,40 @@ __global__ void __launch_bounds__(kThreads) ffn_simt_kernel(const FfnArgs g) {
     griddep_launch_dependents();
 }
 
-cudaError_t launch_ffn_simt(int op, const FfnArgs& a, cudaStream_t st) {
-    const unsigned blocks = static_cast<unsigned>((a.R + kM - 1) / kM + a.n);
-    const unsigned fd = static_cast<unsigned>((a.d + kN - 1) / kN), ff = static_cast<unsigned>((a.F + kN - 1) / kN);
+template <int kOp>
+static cudaError_t launch_row_op(const FfnArgs& a, int column_tiles, int K, int num_sms, cudaStream_t st) {
+    const int64_t blocks = (a.R + kM - 1) / kM + a.n;  // at most
+    const int64_t likely = std::max<int64_t>((a.R + kM - 1) / kM, std::min<int64_t>(a.n, a.R));
+    // up to 4 blocks per SM run together
+    int splits = 1;
+    while (splits < 8 && likely * column_tiles * splits * 2 <= 4 * num_sms && K / kK >= 8 * splits) splits *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks * splits), static_cast<unsigned>(column_tiles));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = (g_chain_started && pdl_enabled()) ? 2 : 1;
+    g_chain_started = true;
+    return cudaLaunchKernelEx(&cfg, ffn_simt_kernel<kOp>, a, splits);
+}
+
+cudaError_t launch_ffn_simt(int op, const FfnArgs& a, int num_sms, cudaStream_t st) {
+    const int fd = (a.d + kN - 1) / kN, ff = (a.F + kN - 1) / kN;
     switch (op) {
-        case kFfnUp:
-            return launch_k(ffn_simt_kernel<kFfnUp>, dim3(blocks, a.F / 64), dim3(kThreads), 0, st, a);
-        case kFfnDown:
-            return launch_k(ffn_simt_kernel<kFfnDown>, dim3(blocks, fd), dim3(kThreads), 0, st, a);
-        case kFfnGrad:
-            return launch_k(ffn_simt_kernel<kFfnGrad>, dim3(blocks, ff), dim3(kThreads), 0, st, a);
-        case kFfnDx:
-            return launch_k(ffn_simt_kernel<kFfnDx>, dim3(blocks, fd), dim3(kThreads), 0, st, a);
+        case kFfnUp: return launch_row_op<kFfnUp>(a, a.F / 64, a.d, num_sms, st);
+        case kFfnDown: return launch_row_op<kFfnDown>(a, fd, a.F, num_sms, st);
+        case kFfnGrad: return launch_row_op<kFfnGrad>(a, ff, a.d, num_sms, st);
+        case kFfnDx: return launch_row_op<kFfnDx>(a, fd, 2 * a.F, num_sms, st);
         case kFfnDw: {
             const unsigned tiles = static_cast<unsigned>(a.d / kM) * (a.F / 64) + static_cast<unsigned>(a.F / kM) * fd;
-            return launch_k(ffn_simt_kernel<kFfnDw>, dim3(tiles, a.n), dim3(kThreads), 0, st, a);
+            return launch_k(ffn_simt_kernel<kFfnDw>, dim3(tiles, a.n), dim3(kThreads), 0, st, a, 1);
         }
     }
     return cudaErrorInvalidValue;

@@ -190,6 +190,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = tail->tmem_base;
     const SegmentPlan& plan = tail->plan;
     const int total = kOp == kFfnDw ? args.n * (args.dw_tiles13 + args.dw_tiles2) : plan.blk[args.n] * args.n_tiles;
+    // this pair's tiles: runs of `run` tiles, dealt round robin
+    const int run = kOp == kFfnDw ? args.dw_run : 1;
+    auto tile_index = [&](int i) { return (i / run * ncl + cid) * run + i % run; };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const CUtensorMap *ma = &tm_a0, *mb = &tm_b0;
             int held = -1;  // kFfnDw: (expert, matrix) whose maps are acquired
             const int r = static_cast<int>(rank);
-            for (int t = cid; t < total && ok; t += ncl) {
+            for (int i = 0, t = cid * run; t < total && ok; t = tile_index(++i)) {
                 const Tile ti = tile_at<kOp>(t, plan, args);
                 if (kOp == kFfnDw && ti.steps > 0 && held != 2 * ti.e + (ti.dw2 ? 1 : 0)) {
                     held = 2 * ti.e + (ti.dw2 ? 1 : 0);
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             int local = 0;
             bool ok = true;
-            for (int t = cid; t < total && ok; t += ncl, ++local) {
+            for (int t = cid * run; t < total && ok; t = tile_index(++local)) {
                 const Tile ti = tile_at<kOp>(t, plan, args);
                 const int buf = local & 1;
                 const uint32_t bph = static_cast<uint32_t>(local >> 1) & 1u;
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const FfnArgs& f = args.f;
         uint8_t* block = smem + kStages * kStageBytes + kTailBytes + (warp - 2) * kExchangeBytes;
         int local = 0;
-        for (int t = cid; t < total; t += ncl, ++local) {
+        for (int t = cid * run; t < total; t = tile_index(++local)) {
             const Tile ti = tile_at<kOp>(t, plan, args);
             const int buf = local & 1;
             const uint32_t bph = static_cast<uint32_t>(local >> 1) & 1u;
@@ -422,21 +425,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int col0 = kOp == kFfnDw && !ti.dw2 ? ti.n_tile * 128 : ti.n_tile * kBN + half * 128;
                 const int64_t base =
                     (kOp == kFfnDw ? static_cast<int64_t>(ti.e) * args.d * args.F : 0) + row * cols + col0;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    if (col0 + c * 32 >= cols) break;
-                    uint32_t v[32], w[16];
-                    if (ti.steps > 0) {
-                        tmem_ld_32x32b_x32(tbase + half * 128 + c * 32, v);
-                        tmem_wait_ld();
-                        pack32(v, w);
-                    } else {  // an expert without rows
+                // all columns at once, so that the four loads wait once
+                uint32_t w[4][16];
+                if (ti.steps > 0) {
+                    uint32_t v[4][32];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) w[j] = 0u;
-                    }
-                    exchange_store(block, w, lane, valid, static_cast<uint16_t*>(out) + base + c * 32,
-                                   static_cast<int64_t>(cols) * 2);
+                    for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tbase + half * 128 + c * 32, v[c]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) pack32(v[c], w[c]);
+                } else {  // an expert without rows
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[c][j] = 0u;
                 }
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (col0 + c * 32 < cols)
+                        exchange_store(block, w[c], lane, valid, static_cast<uint16_t*>(out) + base + c * 32,
+                                       static_cast<int64_t>(cols) * 2);
             }
             tc_fence_before();
             __syncwarp();
@@ -530,6 +538,9 @@ cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnArgs& f, con
     if (op == kFfnDw) {
         a.dw_tiles13 = up(f.d, kBM) * up(f.F, 128);
         a.dw_tiles2 = up(f.F, kBM) * up(f.d, kBN);
+        // Few rows per expert make short tiles, for which changing the expert (two
+        // tensor maps to fetch) would cost as much as the tile: runs of 8 then.
+        a.dw_run = f.R <= 512 * static_cast<int64_t>(f.n) ? 8 : 1;
         return launch_op<kFfnDw>(maps, a, static_cast<int64_t>(f.n) * (a.dw_tiles13 + a.dw_tiles2), num_sms, st);
     }
     const int k = op == kFfnUp || op == kFfnGrad ? f.d : (op == kFfnDown ? f.F : 2 * f.F);

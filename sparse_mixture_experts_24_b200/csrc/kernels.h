@@ -382,7 +382,7 @@ struct FfnArgs {
     int* status;
 };
 // fp32 on the CUDA cores (ffn_simt.cu).
-cudaError_t launch_ffn_simt(int op, const FfnArgs& a, cudaStream_t st);
+cudaError_t launch_ffn_simt(int op, const FfnArgs& a, int num_sms, cudaStream_t st);
 
 // bf16 on the tensor cores (gemm_ffn.cu).  maps: A (and A2), B (and B2) of the
 // op -- row operands [R][cols] in 64 x 128 boxes; weights that are N-major
@@ -400,6 +400,7 @@ struct FfnTcArgs {
     int n_tiles;  // column tiles (row ops)
     int band;     // row blocks per band of the tile order
     int dw_tiles13, dw_tiles2;
+    int dw_run;   // consecutive kFfnDw tiles that one CTA pair takes
     const CUtensorMap* maps;
 };
 cudaError_t launch_ffn_maps(const CUtensorMap* maps5, const int32_t* offsets, int n, int64_t R, void* out,

@@ -19,6 +19,7 @@
 //                    both the reads along `out` and the writes along `in` are
 //                    whole sectors.
 // Both are bound by memory: each input is read once, each output written once.
+#include <cuda_fp16.h>
 #include <cuda_fp4.h>
 
 #include <algorithm>
@@ -43,68 +44,93 @@ __device__ __forceinline__ float mx_scale(uint32_t c) {
     return __uint_as_float(c == 0u ? 0x00400000u : c << 23);  // c = 0: 2^-127, a subnormal
 }
 
-// E2M1 code (low four bits) of v times the inverse scale.
-__device__ __forceinline__ uint32_t mx_code(float v, float inverse) {
-    return static_cast<uint32_t>(__nv_cvt_float_to_fp4(v * inverse, __NV_E2M1, cudaRoundNearest)) & 0xFu;
+// E2M1 codes of two values (a in the low four bits) and what two codes stand for
+// (exact in fp16).
+__device__ __forceinline__ uint32_t mx_codes2(float a, float b) {
+    return static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(a, b), __NV_E2M1, cudaRoundNearest));
+}
+__device__ __forceinline__ float2 mx_values2(uint32_t codes) {
+    const __half2_raw h =
+        __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(codes & 0xFFu), __NV_E2M1);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Value of an E2M1 code: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.
-__device__ __forceinline__ float mx_value(uint32_t code) {
-    const uint32_t ex = (code >> 1) & 3u, man = code & 1u;
-    const float mag = ex == 0u ? 0.5f * man : __uint_as_float(((ex + 126u) << 23) | (man << 22));
-    return (code & 8u) ? -mag : mag;
+// Eight elements of a block: codes, and in place the values.
+__device__ __forceinline__ uint32_t mx_pack8(float (&v)[8], uint32_t c, bool values) {
+    uint32_t packed = 0u;
+    if (c != 255u) {
+        const float inverse = mx_inverse_scale(c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) packed |= mx_codes2(v[2 * i] * inverse, v[2 * i + 1] * inverse) << (8 * i);
+    }
+    if (values) {
+        const float scale = c == 255u ? __uint_as_float(0x7FC00000u) : mx_scale(c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 q = mx_values2(packed >> (8 * i));
+            v[2 * i] = q.x * scale;
+            v[2 * i + 1] = q.y * scale;
+        }
+    }
+    return packed;
 }
 
-template <bool kBf16>
+// kAhead pieces per thread and round, loaded together: one 16-byte load in
+// flight per thread does not cover the latency of memory at its bandwidth.
+template <bool kBf16, int kAhead>
 __global__ void __launch_bounds__(256) mx_rows_kernel(const void* __restrict__ src, int64_t pieces,
                                                       uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
                                                       void* __restrict__ values) {
     // piece = 8 elements; 4 neighbouring lanes hold one block.  `pieces` is a
     // multiple of 4, so a block is never cut by the end of the array.
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t first = static_cast<int64_t>(blockIdx.x) * blockDim.x; first < pieces; first += step) {
-        const int64_t p = first + threadIdx.x;
-        const bool in = p < pieces;
-        float v[8];
-        if (!in) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (256 * kAhead);
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * kAhead) + threadIdx.x; first - threadIdx.x < pieces;
+         first += step) {
+        uint4 raw[kAhead][kBf16 ? 1 : 2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        } else if (kBf16) {
-            const uint4 q = __ldg(static_cast<const uint4*>(src) + p);
-            unpack_bf16x2(q.x, v[0], v[1]);
-            unpack_bf16x2(q.y, v[2], v[3]);
-            unpack_bf16x2(q.z, v[4], v[5]);
-            unpack_bf16x2(q.w, v[6], v[7]);
-        } else {
-            const float4 a = __ldg(static_cast<const float4*>(src) + 2 * p);
-            const float4 b = __ldg(static_cast<const float4*>(src) + 2 * p + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t p = first + 256 * u;
+#pragma unroll
+            for (int h = 0; h < (kBf16 ? 1 : 2); ++h)
+                raw[u][h] = p < pieces ? __ldg(static_cast<const uint4*>(src) + (kBf16 ? p : 2 * p + h))
+                                       : make_uint4(0u, 0u, 0u, 0u);
         }
-        uint32_t top = 0u;  // magnitudes order like their bit patterns, NaN and infinity above all
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t c = mx_scale_code(top);
-        uint32_t packed = 0u;
-        if (c != 255u) {
-            const float inverse = mx_inverse_scale(c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) packed |= mx_code(v[i], inverse) << (4 * i);
-        }
-        if (!in) continue;
-        reinterpret_cast<uint32_t*>(codes)[p] = packed;
-        if ((p & 3) == 0) scales[p >> 2] = static_cast<uint8_t>(c);
-        if (values) {
-            const float scale = c == 255u ? __uint_as_float(0x7FC00000u) : mx_scale(c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = mx_value((packed >> (4 * i)) & 0xFu) * scale;
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t p = first + 256 * u;
+            float v[8];
             if (kBf16) {
-                static_cast<uint4*>(values)[p] = pack_bf16x8(v);
+                const uint4 q = raw[u][0];
+                unpack_bf16x2(q.x, v[0], v[1]);
+                unpack_bf16x2(q.y, v[2], v[3]);
+                unpack_bf16x2(q.z, v[4], v[5]);
+                unpack_bf16x2(q.w, v[6], v[7]);
             } else {
-                static_cast<float4*>(values)[2 * p] = make_float4(v[0], v[1], v[2], v[3]);
-                static_cast<float4*>(values)[2 * p + 1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+                for (int h = 0; h < (kBf16 ? 1 : 2); ++h) {
+                    const uint4 q = raw[u][h];
+                    v[4 * h] = __uint_as_float(q.x), v[4 * h + 1] = __uint_as_float(q.y);
+                    v[4 * h + 2] = __uint_as_float(q.z), v[4 * h + 3] = __uint_as_float(q.w);
+                }
+            }
+            uint32_t top = 0u;  // magnitudes order like their bit patterns, NaN and infinity above all
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t c = mx_scale_code(top);
+            const uint32_t packed = mx_pack8(v, c, values != nullptr);
+            if (p < pieces) {
+                reinterpret_cast<uint32_t*>(codes)[p] = packed;
+                if ((p & 3) == 0) scales[p >> 2] = static_cast<uint8_t>(c);
+                if (values) {
+                    if (kBf16) {
+                        static_cast<uint4*>(values)[p] = pack_bf16x8(v);
+                    } else {
+                        static_cast<float4*>(values)[2 * p] = make_float4(v[0], v[1], v[2], v[3]);
+                        static_cast<float4*>(values)[2 * p + 1] = make_float4(v[4], v[5], v[6], v[7]);
+                    }
+                }
             }
         }
     }
@@ -138,20 +164,20 @@ __global__ void __launch_bounds__(128) mx_weights_kernel(const void* __restrict_
         top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
     }
     const uint32_t c = mx_scale_code(top);
-    uint32_t packed[4] = {0u, 0u, 0u, 0u};
-    if (c != 255u) {
-        const float inverse = mx_inverse_scale(c);
+    uint32_t packed[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) packed[i >> 3] |= mx_code(v[i], inverse) << (4 * (i & 7));
+    for (int q = 0; q < 4; ++q) {
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = v[8 * q + i];
+        packed[q] = mx_pack8(u, c, values != nullptr);
+        if (values) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s_values[lane][32 * kb + 8 * q + i] = u[i];
+        }
     }
     s_codes[lane][kb] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
     s_scales[lane][kb] = static_cast<uint8_t>(c);
-    if (values) {
-        const float scale = c == 255u ? __uint_as_float(0x7FC00000u) : mx_scale(c);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            s_values[lane][32 * kb + i] = mx_value((packed[i >> 3] >> (4 * (i & 7))) & 0xFu) * scale;
-    }
     __syncthreads();
     const int blocks = min(kMxTileK, rows - k0) / 32;  // `rows` is a multiple of 32
     {
@@ -179,11 +205,13 @@ __global__ void __launch_bounds__(128) mx_weights_kernel(const void* __restrict_
 cudaError_t launch_mx_rows(const void* src, bool bf16, int64_t rows, int cols, uint8_t* codes, uint8_t* scales,
                            void* values, int num_sms, cudaStream_t st) {
     const int64_t pieces = rows * (cols / 8);
-    const int64_t blocks = std::min<int64_t>((pieces + 255) / 256, static_cast<int64_t>(num_sms) * 32);
-    if (bf16)
-        mx_rows_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, st>>>(src, pieces, codes, scales, values);
-    else
-        mx_rows_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, st>>>(src, pieces, codes, scales, values);
+    // four pieces per thread once that still fills every SM with blocks
+    const bool many = pieces >= static_cast<int64_t>(num_sms) * 8 * 256 * 4;
+    const int64_t per = many ? 256 * 4 : 256;
+    const int64_t blocks = std::min<int64_t>((pieces + per - 1) / per, static_cast<int64_t>(num_sms) * 32);
+    auto kernel = bf16 ? (many ? mx_rows_kernel<true, 4> : mx_rows_kernel<true, 1>)
+                       : (many ? mx_rows_kernel<false, 4> : mx_rows_kernel<false, 1>);
+    kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(src, pieces, codes, scales, values);
     return cudaGetLastError();
 }
 
