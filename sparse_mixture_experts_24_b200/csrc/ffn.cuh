@@ -108,6 +108,47 @@ __device__ __forceinline__ void exchange_store(uint8_t* block, const uint32_t* w
     __syncwarp();
 }
 
+// The same through the tensor map of the output (32 x 32 boxes, 64-byte swizzle:
+// the block's own layout), for warps whose 32 rows are all to be stored: a
+// tenth of the load-store unit's work.  Two blocks take turns; `turn` counts
+// the warp's stores.  c0, c1 (, c2): column, row (and expert).
+__device__ __forceinline__ uint8_t* exchange_put(uint8_t* blocks, int& turn, const uint32_t* w, int lane) {
+    uint8_t* block = blocks + (turn++ & 1) * kExchangeBytes;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the block is free again
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *exchange_at(block, lane, q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    return block;
+}
+__device__ __forceinline__ void exchange_send_2d(uint8_t* blocks, int& turn, const uint32_t* w, int lane,
+                                                 const CUtensorMap* map, int c0, int c1) {
+    const uint32_t src = smem_u32(exchange_put(blocks, turn, w, lane));
+    if (lane == 0)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+            "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+            "r"(c0), "r"(c1), "r"(src)
+            : "memory");
+}
+__device__ __forceinline__ void exchange_send_3d(uint8_t* blocks, int& turn, const uint32_t* w, int lane,
+                                                 const CUtensorMap* map, int c0, int c1, int c2) {
+    const uint32_t src = smem_u32(exchange_put(blocks, turn, w, lane));
+    if (lane == 0)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+            "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+            "r"(c0), "r"(c1), "r"(c2), "r"(src)
+            : "memory");
+}
+// Before another use of the blocks, and before the warp ends: every store that
+// this lane has sent is complete.
+__device__ __forceinline__ void exchange_drain() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void exchange_drain_reads() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 // The two halves of a load: fetch (in flight until its registers are used) and
 // the turn to one row per lane.  Rows past `valid` read zeros.
 __device__ __forceinline__ void exchange_fetch(uint4 (&v)[4], int lane, int valid, const void* src, int64_t ld_bytes) {

@@ -149,6 +149,22 @@ bool map_weights(CUtensorMap* m, const void* p, int n, int rows, int cols) {
     return encode_bf16(m, p, 3, dims, strides, box);
 }
 
+// Outputs: 32 rows x 32 columns per store, of rows [rows][cols] or of weight
+// gradients [n][rows][cols] (rows past the matrix are clipped).
+bool map_out(CUtensorMap* m, const void* p, int64_t rows, int cols) {
+    const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(cols) * 2};
+    const uint32_t box[2] = {32, 32};
+    return moe_api_detail::encode_bf16_64(m, p, 2, dims, strides, box);
+}
+bool map_out_weights(CUtensorMap* m, const void* p, int n, int rows, int cols) {
+    const uint64_t r = rows, c = cols;
+    const uint64_t dims[3] = {c, r, static_cast<uint64_t>(n)};
+    const uint64_t strides[2] = {c * 2, r * c * 2};
+    const uint32_t box[3] = {32, 32, 1};
+    return moe_api_detail::encode_bf16_64(m, p, 3, dims, strides, box);
+}
+
 moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t st, const char* what) {
     cudaError_t e;
     if (v.bf16) {
@@ -166,9 +182,23 @@ moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t 
         else if (op == moe::kFfnDx)
             ok = map_rows(&m[0], a.da, a.R, F, box) && map_rows(&m[1], a.db, a.R, F, box) &&
                  map_weights(&m[2], a.w1, n, d, F) && map_weights(&m[3], a.w3, n, d, F);
+        moe::FfnOutMaps out = {};
+        if (few || !ok)
+            ;  // no output maps
+        else if (op == moe::kFfnUp)
+            ok = map_out(&out.m[0], a.h, a.R, F) &&
+                 (!a.gate || (map_out(&out.m[1], a.gate, a.R, F) && map_out(&out.m[2], a.up, a.R, F)));
+        else if (op == moe::kFfnGrad)
+            ok = map_out(&out.m[0], a.da, a.R, F) && map_out(&out.m[1], a.db, a.R, F) &&
+                 map_out(&out.m[2], a.h, a.R, F);
+        else if (op == moe::kFfnDw)
+            ok = map_out_weights(&out.m[0], a.dw1, n, d, F) && map_out_weights(&out.m[1], a.dw3, n, d, F) &&
+                 map_out_weights(&out.m[2], a.dw2, n, F, d);
+        else
+            ok = map_out(&out.m[0], op == moe::kFfnDown ? a.y : a.dx, a.R, d);
         if (!ok) return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%s)", what);
         e = few ? moe::launch_ffn_few(op, few, m, a, v.num_sms, st)
-                : moe::launch_ffn_tc(op, m, a, v.ffn->maps, v.num_sms, st);
+                : moe::launch_ffn_tc(op, m, out, a, v.ffn->maps, v.num_sms, st);
     } else {
         e = moe::launch_ffn_simt(op, a, v.num_sms, st);
     }
@@ -405,15 +435,52 @@ moe_status moe_matmul_mxfp4(moe_handle* h, int64_t R, int N, int K, const int32_
     const uint32_t a_box[2] = {128, static_cast<uint32_t>(moe::mx_gemm_tile_rows(R, v.n))};
     const uint64_t w_dims[3] = {k2, cols, static_cast<uint64_t>(v.n)}, w_strides[2] = {k2, k2 * cols};
     const uint32_t w_box[3] = {128, 128, 1};
-    CUtensorMap m[3] = {};
+    CUtensorMap m[5] = {};
+    // out in boxes of 32 rows x 64 bytes, where its rows allow a map
+    const int per16 = v.bf16 ? 8 : 4;
+    const uint64_t o_dims[2] = {cols, static_cast<uint64_t>(R)}, o_strides[1] = {cols * (v.bf16 ? 2 : 4)};
+    const uint32_t o_box[2] = {v.bf16 ? 32u : 16u, 32};
+    if (N % per16 == 0 && !(v.bf16 ? moe_api_detail::encode_bf16_64(&m[3], out, 2, o_dims, o_strides, o_box)
+                                   : moe_api_detail::encode_f32_64(&m[3], out, 2, o_dims, o_strides, o_box)))
+        return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (MXFP4 product)");
     if (!moe_api_detail::encode_bytes(&m[0], a_codes, 2, a_dims, a_strides, a_box) ||
         !moe_api_detail::encode_bytes(&m[1], w_codes, 3, w_dims, w_strides, w_box) ||
         (pair_codes && !moe_api_detail::encode_bytes(&m[2], pair_codes, 3, w_dims, w_strides, w_box)))
         return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (MXFP4 product)");
+    // Pairs need scratch for the scales.  Where it cannot be had because the stream
+    // is captured, the other kernel takes the call: the same products in the same
+    // order.
+    bool pairs = moe::mx_gemm_uses_pairs(a, v.num_sms);
+    moe::MxChunks ch{};
+    if (pairs) {
+        ch = moe::mx_gemm_chunks(a);
+        const int64_t rows = ch.blocks * ch.steps;
+        if (rows * 1024 > v.ffn->chunk_bytes) {
+            cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+            cudaError_t e = cudaStreamIsCapturing(st, &cap);
+            if (e != cudaSuccess) {
+                cudaGetLastError();
+                return cuda_failed(e, "cudaStreamIsCapturing");
+            }
+            if (cap != cudaStreamCaptureStatusNone) {
+                pairs = false;
+            } else {
+                s = allocate(v.ffn, static_cast<size_t>(rows) * 1024, st, true, &v.ffn->chunks);
+                if (s != MOE_OK) return s;
+                v.ffn->chunk_bytes = rows * 1024;
+            }
+        }
+        ch.base = static_cast<uint8_t*>(v.ffn->chunks);
+        const uint64_t c_dims[2] = {256, static_cast<uint64_t>(rows)}, c_strides[1] = {1024};
+        const uint32_t c_box[2] = {256, 1};
+        if (pairs && !moe_api_detail::encode_words(&m[4], ch.base, 2, c_dims, c_strides, c_box))
+            return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (MXFP4 scales)");
+    }
     moe::chain_begin();
-    cudaError_t e = moe::launch_mx_gemm(m, a, v.bf16, v.num_sms, st);
+    cudaError_t e = pairs ? moe::launch_mx_gemm_pairs(m, a, v.bf16, ch, v.num_sms, st)
+                          : moe::launch_mx_gemm(m, a, v.bf16, v.num_sms, st);
     if (e != cudaSuccess) return cuda_failed(e, "MXFP4 product launch");
-    *v.launches += 1;
+    *v.launches += pairs ? 2 : 1;
     return done();
 }
 

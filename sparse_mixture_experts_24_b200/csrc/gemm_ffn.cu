@@ -20,7 +20,11 @@
 //   warp 1     of the leader: tcgen05.mma.cta_group::2 (M 256, N 256, K 16);
 //   warps 2-9  epilogue, two per 32 accumulator rows, each on half the columns:
 //              the block's elementwise part on the fp32 accumulators, bf16
-//              rows through the warp's exchange block (ffn.cuh).  Two accumulators (512 TMEM columns): a tile's epilogue
+//              rows through the warp's exchange blocks (ffn.cuh), by TMA where
+//              all 32 rows are stored.  128 experts of 2,048 x 768 with 128 rows
+//              each: storing 16 bytes per lane straight from registers, dw took
+//              628 us; 64-byte segments through the blocks 442 us, by
+//              TMA 286 us.  Two accumulators (512 TMEM columns): a tile's epilogue
 //              runs under the next tile's products.
 // kFfnDx adds both of its products in one accumulator: K simply runs over da
 // with w1 and then db with w3.  kFfnDw does all three weight gradients in one
@@ -57,8 +61,10 @@ struct __align__(16) Tail {
     uint32_t tmem_base;
     SegmentPlan plan;
 };
-constexpr int kTailBytes = (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128;
-constexpr int kSmemBytes = kStages * kStageBytes + kTailBytes + kEpiWarps * kExchangeBytes + 1024;
+// Shared memory, 1 KB aligned: barriers and plan, the ring, two exchange blocks
+// per epilogue warp.
+constexpr int kTailBytes = (static_cast<int>(sizeof(Tail)) + 1023) / 1024 * 1024;
+constexpr int kSmemBytes = kTailBytes + kStages * kStageBytes + 2 * kEpiWarps * kExchangeBytes;
 static_assert(kSmemBytes <= 232448, "shared memory");
 
 struct Tile {
@@ -129,6 +135,14 @@ __device__ __forceinline__ Tile tile_at(int t, const SegmentPlan& p, const FfnTc
 
 __device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.f, 1.f + __expf(-a)); }
 
+// Hand an accumulator back to the leader's MMA thread.  Relaxed: what has to
+// come before it are the warp's tensor-memory loads, which tcgen05.wait::ld has
+// completed.  A release at cluster scope would also wait for the warp's global
+// stores of the tile.
+__device__ __forceinline__ void hand_back_to(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 __device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
     asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map))
                  : "memory");
@@ -148,13 +162,12 @@ template <int kOp>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_tc_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
                   const __grid_constant__ CUtensorMap tm_b0, const __grid_constant__ CUtensorMap tm_b1,
-                  const FfnTcArgs args) {
+                  const __grid_constant__ FfnOutMaps tm_out, const FfnTcArgs args) {
     constexpr bool kAMn = kOp == kFfnDw;                      // A is M-major in shared memory
     constexpr bool kBMn = kOp != kFfnGrad && kOp != kFfnDx;   // B is N-major
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~static_cast<uintptr_t>(1023));
-    Tail* tail = reinterpret_cast<Tail*>(smem + kStages * kStageBytes);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Tail* tail = reinterpret_cast<Tail*>(smem_raw);
+    uint8_t* smem = smem_raw + kTailBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int cid = static_cast<int>(cluster_id_x()), ncl = static_cast<int>(nclusters_x());
@@ -323,7 +336,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t hand_back[2] = {mapa_shared(smem_u32(&tail->accum_empty[0]), 0),
                                        mapa_shared(smem_u32(&tail->accum_empty[1]), 0)};
         const FfnArgs& f = args.f;
-        uint8_t* block = smem + kStages * kStageBytes + kTailBytes + (warp - 2) * kExchangeBytes;
+        uint8_t* block = smem + kStages * kStageBytes + (warp - 2) * (2 * kExchangeBytes);
+        int turn = 0;
+        // 32 columns of this warp's rows to one output: through its tensor map where
+        // all 32 rows are stored, else row by row
+        auto store = [&](const uint32_t* w, int which, void* out, int64_t row, int cols, int col, int valid) {
+            if (valid == 32) {
+                exchange_send_2d(block, turn, w, lane, &tm_out.m[which], col, static_cast<int>(row));
+            } else {
+                if (lane == 0) exchange_drain_reads();
+                __syncwarp();
+                exchange_store(block, w, lane, valid, static_cast<uint16_t*>(out) + row * cols + col, cols * 2LL);
+            }
+        };
         int local = 0;
         for (int t = cid * run; t < total; t = tile_index(++local)) {
             const Tile ti = tile_at<kOp>(t, plan, args);
@@ -345,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r0 = 128 * static_cast<int>(rank) + 32 * quad;  // this warp's 32 rows of the tile
             const int valid = min(32, ti.rows - r0);                 // warp-uniform, like every column test
             const int64_t row = static_cast<int64_t>(ti.row0) + r0;
+            bool returned = false;  // the accumulator
             if (valid <= 0) {
                 // nothing of this warp's to store
             } else if (kOp == kFfnUp) {
@@ -357,12 +383,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld_32x32b_x32(tbase + at, a);
                     tmem_ld_32x32b_x32(tbase + 128 + at, b);
                     tmem_wait_ld();
-                    const int64_t o = (row * args.F + col) * 2, ld = static_cast<int64_t>(args.F) * 2;
                     if (f.gate) {
                         pack32(a, w);
-                        exchange_store(block, w, lane, valid, static_cast<uint8_t*>(f.gate) + o, ld);
+                        store(w, 1, f.gate, row, args.F, col, valid);
                         pack32(b, w);
-                        exchange_store(block, w, lane, valid, static_cast<uint8_t*>(f.up) + o, ld);
+                        store(w, 2, f.up, row, args.F, col, valid);
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -374,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         w[j] = pack_bf16x2(h[0], h[1]);
                     }
-                    exchange_store(block, w, lane, valid, static_cast<uint8_t*>(f.h) + o, ld);
+                    store(w, 0, f.h, row, args.F, col, valid);
                 }
             } else if (kOp == kFfnGrad) {
                 // the first chunk of gate and up was fetched before the wait for the
@@ -388,6 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int64_t o = (row * args.F + col) * 2;
                     uint32_t ga[16], gb[16], dh[32];
                     tmem_ld_32x32b_x32(tbase + at, dh);
+                    if (lane == 0) exchange_drain_reads();
+                    __syncwarp();
                     exchange_turn(block, gate_next, lane, ga);
                     exchange_turn(block, up_next, lane, gb);
                     if (c < 3 && col + 32 < args.F) {
@@ -413,18 +440,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         gb[j] = pack_bf16x2(y[0], y[1]);
                         hw[j] = pack_bf16x2(h[0], h[1]);
                     }
-                    exchange_store(block, ga, lane, valid, static_cast<uint8_t*>(f.da) + o, ld);
-                    exchange_store(block, gb, lane, valid, static_cast<uint8_t*>(f.db) + o, ld);
-                    exchange_store(block, hw, lane, valid, static_cast<uint8_t*>(f.h) + o, ld);
+                    store(ga, 0, f.da, row, args.F, col, valid);
+                    store(gb, 1, f.db, row, args.F, col, valid);
+                    store(hw, 2, f.h, row, args.F, col, valid);
                 }
             } else {
                 // Down, Dx: columns of y or dx.  Dw: half 0 of a dw1 | dw3 tile is
-                // dw1's columns, half 1 dw3's; dw2 tiles are 256 columns wide.
-                void* out = kOp == kFfnDown ? f.y : (kOp == kFfnDx ? f.dx : (ti.dw2 ? f.dw2 : (half ? f.dw3 : f.dw1)));
+                // dw1's columns, half 1 dw3's; dw2 tiles are 256 columns wide, and
+                // every warp has 32 rows or none (d and F are multiples of 64).
                 const int cols = kOp == kFfnDw && !ti.dw2 ? args.F : args.d;
                 const int col0 = kOp == kFfnDw && !ti.dw2 ? ti.n_tile * 128 : ti.n_tile * kBN + half * 128;
-                const int64_t base =
-                    (kOp == kFfnDw ? static_cast<int64_t>(ti.e) * args.d * args.F : 0) + row * cols + col0;
                 // all columns at once, so that the four loads wait once
                 uint32_t w[4][16];
                 if (ti.steps > 0) {
@@ -440,16 +465,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) w[c][j] = 0u;
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) hand_back_to(hand_back[buf]);
+                returned = true;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (col0 + c * 32 < cols)
-                        exchange_store(block, w[c], lane, valid, static_cast<uint16_t*>(out) + base + c * 32,
-                                       static_cast<int64_t>(cols) * 2);
+                for (int c = 0; c < 4; ++c) {
+                    const int col = col0 + c * 32;
+                    if (col >= cols) break;
+                    if (kOp == kFfnDw)
+                        exchange_send_3d(block, turn, w[c], lane, &tm_out.m[ti.dw2 ? 2 : half], col,
+                                         static_cast<int>(row), ti.e);
+                    else
+                        store(w[c], 0, kOp == kFfnDown ? f.y : f.dx, row, args.d, col, valid);
+                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(hand_back[buf]);
+            if (!returned) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) hand_back_to(hand_back[buf]);
+            }
         }
+        if (lane == 0) exchange_drain();
     }
 
     tc_fence_before();
@@ -502,7 +539,7 @@ cudaError_t launch_ffn_maps(const CUtensorMap* maps5, const int32_t* offsets, in
 }
 
 template <int kOp>
-static cudaError_t launch_op(const CUtensorMap* m, const FfnTcArgs& a, int64_t max_tiles, int num_sms,
+static cudaError_t launch_op(const CUtensorMap* m, const FfnOutMaps& out, const FfnTcArgs& a, int64_t max_tiles, int num_sms,
                              cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<kOp>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -523,11 +560,11 @@ static cudaError_t launch_op(const CUtensorMap* m, const FfnTcArgs& a, int64_t m
     cfg.attrs = attr;
     cfg.numAttrs = (g_chain_started && pdl_enabled()) ? 2 : 1;
     g_chain_started = true;
-    return cudaLaunchKernelEx(&cfg, ffn_tc_kernel<kOp>, m[0], m[1], m[2], m[3], a);
+    return cudaLaunchKernelEx(&cfg, ffn_tc_kernel<kOp>, m[0], m[1], m[2], m[3], out, a);
 }
 
-cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnArgs& f, const void* dw_maps, int num_sms,
-                          cudaStream_t st) {
+cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnOutMaps& out, const FfnArgs& f,
+                          const void* dw_maps, int num_sms, cudaStream_t st) {
     FfnTcArgs a{};
     a.f = f;
     a.n = f.n;
@@ -541,7 +578,7 @@ cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnArgs& f, con
         // Few rows per expert make short tiles, for which changing the expert (two
         // tensor maps to fetch) would cost as much as the tile: runs of 8 then.
         a.dw_run = f.R <= 512 * static_cast<int64_t>(f.n) ? 8 : 1;
-        return launch_op<kFfnDw>(maps, a, static_cast<int64_t>(f.n) * (a.dw_tiles13 + a.dw_tiles2), num_sms, st);
+        return launch_op<kFfnDw>(maps, out, a, static_cast<int64_t>(f.n) * (a.dw_tiles13 + a.dw_tiles2), num_sms, st);
     }
     const int k = op == kFfnUp || op == kFfnGrad ? f.d : (op == kFfnDown ? f.F : 2 * f.F);
     a.steps = k / kBK;
@@ -551,10 +588,10 @@ cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnArgs& f, con
     a.band = static_cast<int>(band < 1 ? 1 : band);
     const int64_t tiles = ((f.R + kBM - 1) / kBM + f.n) * static_cast<int64_t>(a.n_tiles);
     switch (op) {
-        case kFfnUp: return launch_op<kFfnUp>(maps, a, tiles, num_sms, st);
-        case kFfnDown: return launch_op<kFfnDown>(maps, a, tiles, num_sms, st);
-        case kFfnGrad: return launch_op<kFfnGrad>(maps, a, tiles, num_sms, st);
-        case kFfnDx: return launch_op<kFfnDx>(maps, a, tiles, num_sms, st);
+        case kFfnUp: return launch_op<kFfnUp>(maps, out, a, tiles, num_sms, st);
+        case kFfnDown: return launch_op<kFfnDown>(maps, out, a, tiles, num_sms, st);
+        case kFfnGrad: return launch_op<kFfnGrad>(maps, out, a, tiles, num_sms, st);
+        case kFfnDx: return launch_op<kFfnDx>(maps, out, a, tiles, num_sms, st);
     }
     return cudaErrorInvalidValue;
 }

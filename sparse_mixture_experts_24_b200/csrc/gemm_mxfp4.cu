@@ -443,7 +443,436 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// ---------------------------------------------------------------------------
+// The same on CTA pairs (cta_group::2) for many rows per expert: 256 x 256
+// tiles, each CTA its own 128 rows and 128 of the columns.
+// ---------------------------------------------------------------------------
+// A 128 x 256 tile brings 48 KB of codes for the 510 cycles of its four MMAs,
+// more than an SM gets from L2 in that time; a pair's CTA brings 32 KB for the
+// same products.  What differs from mx_gemm_kernel:
+//   - the leader's MMA thread issues the pair's copies and MMAs; a copy moves
+//     either CTA's own shared memory into its own tensor memory: the scales of
+//     its rows, and of all 256 columns;
+//   - the scales are turned over before, by mx_scales_kernel, into the chunks
+//     that the tensor core takes, 1 KB per 128 rows (or columns) and step, and
+//     arrive by bulk copies.  Fetched by warps of this kernel from the rows, 8 to
+//     16 bytes at a time, they bound it (8,192 rows over 8 experts, 4,096 x
+//     14,336 twice: 724 to 1,641 us by four ways of fetching them);
+//   - outputs leave by TMA through the warps' exchange blocks where all 32 rows
+//     are stored and a row of out is a multiple of 16 bytes.
+namespace mxp {
+
+constexpr int kStages = 5;
+constexpr int kCodeBytes = 2 * 128 * 128;             // 128 rows, 128 columns
+constexpr int kStageBytes = kCodeBytes + 3 * kSfBytes;  // scales of 128 rows, 256 columns
+constexpr int kSfCols = 24, kSfBase = 256;
+constexpr int kTileRows = 256;
+constexpr int kCopyWarp = 2 + kEpiWarps;
+constexpr int kThreads = (kCopyWarp + 1) * 32;
+constexpr int kChunk = 1024;                          // a step's scales of 128 rows or columns
+
+struct __align__(16) Tail {
+    uint64_t full[kStages];
+    uint64_t empty[kStages];
+    uint64_t scales[kStages];  // in tensor memory
+    uint64_t copied;
+    uint64_t accum_full;
+    uint64_t accum_empty;
+    uint64_t done;
+    uint32_t tmem_base;
+    SegmentPlan plan;
+};
+// Shared memory, 1 KB aligned: barriers and plan, the ring, two exchange blocks
+// per epilogue warp.
+constexpr int kTailBytes = (static_cast<int>(sizeof(Tail)) + 1023) / 1024 * 1024;
+constexpr int kSmemBytes = kTailBytes + kStages * kStageBytes + 2 * kEpiWarps * kExchangeBytes;
+static_assert(kSmemBytes <= 232448 && kStageBytes % 1024 == 0 && kSfBase + kStages * kSfCols <= kTmemCols, "budget");
+
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                    uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+
+}  // namespace mxp
+
+template <bool kPair, bool kBf16Out>
+__global__ void __launch_bounds__(mxp::kThreads, 1)
+    mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                        const __grid_constant__ CUtensorMap tm_b2, const __grid_constant__ CUtensorMap tm_out,
+                        const __grid_constant__ CUtensorMap tm_chunks, const MxGemmArgs args, const MxChunks ch,
+                        const int out_by_map) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    mxp::Tail* tail = reinterpret_cast<mxp::Tail*>(smem_raw);
+    uint8_t* smem = smem_raw + mxp::kTailBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    constexpr int kColsOut = kPair ? 128 : 256;  // output columns of a tile
+    const int n_tiles = (args.N + kColsOut - 1) / kColsOut;
+    const int steps = (args.K + kBK - 1) / kBK;
+    int* status = args.status;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < mxp::kStages; ++s) {
+            mbar_init(smem_u32(&tail->full[s]), 1);
+            mbar_init(smem_u32(&tail->empty[s]), 1);
+            mbar_init(smem_u32(&tail->scales[s]), 1);
+        }
+        mbar_init(smem_u32(&tail->copied), 1);
+        mbar_init(smem_u32(&tail->accum_full), 1);
+        mbar_init(smem_u32(&tail->accum_empty), 2 * kEpiWarps);
+        mbar_init(smem_u32(&tail->done), 1);
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tm_a);
+        tma_prefetch_desc(&tm_b);
+        if (kPair) tma_prefetch_desc(&tm_b2);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&tail->tmem_base), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    griddep_wait();
+    load_plan(tail->plan, args.offsets, args.n, args.R, mxp::kTileRows, status);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any remote arrive
+    tc_fence_after();
+    const uint32_t tmem_base = tail->tmem_base;
+    const SegmentPlan& plan = tail->plan;
+    const int total = plan.blk[args.n] * n_tiles;
+    const int first = static_cast<int>(cluster_id_x()), stride = static_cast<int>(nclusters_x());
+    const int r128 = 128 * static_cast<int>(rank);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer (both CTAs) ----------------
+            int stage = 0;
+            uint32_t phase = 0;
+            int armed[mxp::kStages];
+            for (int s = 0; s < mxp::kStages; ++s) armed[s] = -1;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += stride) {
+                const Tile ti = tile_at<mxp::kTileRows>(t, plan, args.n, n_tiles);
+                // this CTA's 128 rows, and the tile's two blocks of 128 columns
+                const int m = (ti.row0 - plan.off[ti.e]) / mxp::kTileRows;
+                const int sa = ((plan.blk[ti.e] + m) * 2 + static_cast<int>(rank)) * steps;
+                const int cols = ch.a_blocks + ti.e * ch.col_blocks;
+                const int c0 = kPair ? ti.n_tile : 2 * ti.n_tile;
+                const int sb0 = (cols + c0) * steps;
+                // a last, lone block of columns: the second one's outputs are not stored
+                const int sb1 = (kPair ? cols + args.n * ch.col_blocks + c0
+                                       : cols + min(c0 + 1, ch.col_blocks - 1)) * steps;
+                for (int ks = 0; ks < steps; ++ks) {
+                    if (!mbar_wait(smem_u32(&tail->empty[stage]), phase ^ 1u, status, kStatusTimeoutEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full_local = smem_u32(&tail->full[stage]);
+                    if (rank == 0) {
+                        mbar_arrive_expect_tx(full_local, 2 * mxp::kStageBytes);
+                        armed[stage] = static_cast<int>(phase);
+                    }
+                    const uint32_t full = mapa_shared(full_local, 0);
+                    const uint32_t base = smem_u32(smem + stage * mxp::kStageBytes);
+                    tma_load_2d_pair(base, &tm_a, full, ks * 128, ti.row0 + r128);
+                    tma_load_3d_pair(base + kBBlockBytes, kPair && rank ? &tm_b2 : &tm_b, full, ks * 128,
+                                     kPair ? ti.n_tile * 128 : ti.n_tile * 256 + r128, ti.e);
+                    const uint32_t sf = base + mxp::kCodeBytes;
+                    tma_load_2d_pair(sf, &tm_chunks, full, 0, sa + ks);
+                    tma_load_2d_pair(sf + mxp::kChunk, &tm_chunks, full, 0, sb0 + ks);
+                    tma_load_2d_pair(sf + 2 * mxp::kChunk, &tm_chunks, full, 0, sb1 + ks);
+                    if (++stage == mxp::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // the leader's barriers count both CTAs' copies: nothing may still be
+            // landing when the pair exits
+            if (rank == 0)
+                for (int s = 0; s < mxp::kStages; ++s)
+                    if (armed[s] >= 0)
+                        mbar_wait(smem_u32(&tail->full[s]), static_cast<uint32_t>(armed[s]), status,
+                                  kStatusTimeoutDrain);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------- MMA issuer (leader) ----------------
+            int stage = 0;
+            uint32_t phase = 0, use = 0;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += stride, ++use) {
+                if (!mbar_wait(smem_u32(&tail->accum_empty), (use & 1u) ^ 1u, status, kStatusTimeoutAccum)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int ks = 0; ks < steps; ++ks) {
+                    // the stage's scales are in tensor memory, so its codes have landed too
+                    if (!mbar_wait(smem_u32(&tail->scales[stage]), phase, status, kStatusTimeoutFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t base = smem_u32(smem + stage * mxp::kStageBytes);
+                    const uint32_t sf = tmem_base + static_cast<uint32_t>(mxp::kSfBase + stage * mxp::kSfCols);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const int c = kk >> 1;
+                        const uint64_t ad = make_smem_desc(base + kk * 32, 16, 1024, 2);
+                        const uint64_t bd = make_smem_desc(base + kBBlockBytes + kk * 32, 16, 1024, 2);
+                        mxp::mma(tmem_base, ad, bd, (kk & 1) ? idesc_mxf4(256, 256, 2) : idesc_mxf4(256, 256, 0),
+                                 sf + 4 * c, sf + 8 + 8 * c, (ks | kk) != 0 ? 1u : 0u);
+                    }
+                    const uint32_t eb = smem_u32(&tail->empty[stage]);
+                    tc_commit_pair(mapa_shared(eb, 0));
+                    tc_commit_pair(mapa_shared(eb, 1));
+                    if (++stage == mxp::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) {
+                    const uint32_t fb = smem_u32(&tail->accum_full);
+                    tc_commit_pair(mapa_shared(fb, 0));
+                    tc_commit_pair(mapa_shared(fb, 1));
+                }
+            }
+            tc_commit_pair(mapa_shared(smem_u32(&tail->done), 0));
+            mbar_wait(smem_u32(&tail->done), 0, status, kStatusTimeoutDrain);
+        }
+    } else if (warp == mxp::kCopyWarp) {
+        if (lane == 0 && rank == 0) {
+            // ---------------- scales into tensor memory (leader) ----------------
+            // A stage's columns are written again only after its next full barrier,
+            // which follows the MMAs that read them.
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += stride) {
+                for (int ks = 0; ks < steps; ++ks) {
+                    if (!mbar_wait(smem_u32(&tail->full[stage]), phase, status, kStatusTimeoutFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sf_smem = smem_u32(smem + stage * mxp::kStageBytes) + mxp::kCodeBytes;
+                    const uint32_t sf = tmem_base + static_cast<uint32_t>(mxp::kSfBase + stage * mxp::kSfCols);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        mxp::copy_scales(sf + 4 * c, make_smem_desc(sf_smem + c * 512, 0, 128, 0));
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+                            mxp::copy_scales(sf + 8 + 4 * (2 * c + b),
+                                             make_smem_desc(sf_smem + (1 + b) * kSfBytes + c * 512, 0, 128, 0));
+                    }
+                    tc_commit_pair(mapa_shared(smem_u32(&tail->scales[stage]), 0));
+                    if (++stage == mxp::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            tc_commit_pair(mapa_shared(smem_u32(&tail->copied), 0));
+            mbar_wait(smem_u32(&tail->copied), 0, status, kStatusTimeoutDrain);
+        }
+    } else {
+        // ---------------- epilogue (warps 2..9 of both CTAs) ----------------
+        const int quad = warp & 3;         // TMEM lanes 32 * quad .. + 31
+        const int half = (warp - 2) >> 2;  // accumulator columns 128 * half .. (a pair: 64 * half of either)
+        uint8_t* block = smem + mxp::kStages * mxp::kStageBytes + (warp - 2) * (2 * kExchangeBytes);
+        const uint32_t hand_back = mapa_shared(smem_u32(&tail->accum_empty), 0);
+        int turn = 0;
+        uint32_t use = 0;
+        for (int t = first; t < total; t += stride, ++use) {
+            const Tile ti = tile_at<mxp::kTileRows>(t, plan, args.n, n_tiles);
+            if (!mbar_wait(smem_u32(&tail->accum_full), use & 1u, status, kStatusTimeoutAccum)) break;
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+            const int valid = min(32, ti.rows - r128 - quad * 32);  // warp-uniform
+            const int64_t row0 = static_cast<int64_t>(ti.row0) + r128 + quad * 32;
+            uint32_t acc[4][32];
+            if (valid > 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmem_ld_32x32b_x32(
+                        tbase + (kPair ? half * 64 + (i >> 1) * 32 + (i & 1) * 128 : half * 128 + i * 32), acc[i]);
+                tmem_wait_ld();
+            }
+            // relaxed: the loads above are complete, and nothing else has to be
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(hand_back)
+                             : "memory");
+            if (valid > 0) {
+#pragma unroll
+                for (int i = 0; i < (kPair ? 2 : 4); ++i) {
+                    const int col = kPair ? ti.n_tile * 128 + half * 64 + i * 32 : ti.n_tile * 256 + half * 128 + i * 32;
+                    if (col >= args.N) break;
+                    uint32_t(&v)[32] = acc[kPair ? 2 * i : i];
+                    if (kPair) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = __float_as_uint(silu<kBf16Out>(__uint_as_float(v[j])) *
+                                                   __uint_as_float(acc[(2 * i + 1) & 3][j]));
+                    }
+                    if (out_by_map && valid == 32) {
+                        if (kBf16Out) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                v[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                            exchange_send_2d(block, turn, v, lane, &tm_out, col, static_cast<int>(row0));
+                        } else {
+                            exchange_send_2d(block, turn, v, lane, &tm_out, col, static_cast<int>(row0));
+                            if (col + 16 < args.N)
+                                exchange_send_2d(block, turn, v + 16, lane, &tm_out, col + 16, static_cast<int>(row0));
+                        }
+                    } else {
+                        if (lane == 0) exchange_drain_reads();
+                        __syncwarp();
+                        store_rows<kBf16Out>(block, args.out, row0, valid, lane, args.N, col, v);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        if (lane == 0) exchange_drain();
+    }
+
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();  // no remote arrive or commit may target a CTA that has left
+    griddep_launch_dependents();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, kTmemCols);
+    }
+}
+
+// Scales [rows][nb] -> chunks [128-row block][step][1024]: per 128 of K (half a
+// step) 512 bytes with row r's four at 16 (r % 32) + 4 (r / 32).  One block of
+// threads per 128-row block: of A (in the order of the product's row tiles), then
+// of W, then of P.
+__global__ void __launch_bounds__(256) mx_scales_kernel(const MxGemmArgs args, const MxChunks ch) {
+    __shared__ SegmentPlan plan;
+    griddep_wait();
+    load_plan(plan, args.offsets, args.n, args.R, mxp::kTileRows, args.status);
+    griddep_launch_dependents();
+    const int nb = args.K / 32, steps = ch.steps;
+    int64_t block = blockIdx.x;
+    uint8_t* dst = ch.base + block * steps * mxp::kChunk;
+    const uint8_t* src;  // the block's first row, and how many it has
+    int rows;
+    if (block < ch.a_blocks) {
+        const int tile = static_cast<int>(block / 2);
+        if (tile >= plan.blk[args.n]) return;
+        const int e = plan_expert(plan, args.n, tile);
+        const int64_t row = static_cast<int64_t>(plan.off[e]) + static_cast<int64_t>(tile - plan.blk[e]) * mxp::kTileRows +
+                            128 * (block & 1);
+        rows = static_cast<int>(min(static_cast<int64_t>(128), plan.off[e + 1] - row));
+        src = args.a_scales + row * nb;
+    } else {
+        block -= ch.a_blocks;
+        const int64_t own = static_cast<int64_t>(args.n) * ch.col_blocks;
+        const bool second = block >= own;
+        if (second) block -= own;
+        const int64_t e = block / ch.col_blocks;
+        const int64_t col = (block - e * ch.col_blocks) * 128;
+        rows = static_cast<int>(min(static_cast<int64_t>(128), args.N - col));
+        src = (second ? args.b2_scales : args.b_scales) + (e * args.N + col) * nb;
+    }
+    // four neighbouring lanes read 32 bytes of one row together (four steps), and
+    // a warp eight rows
+    const int w = threadIdx.x & 3;
+    for (int i = threadIdx.x >> 2; i < 128 * ((steps + 3) / 4); i += 64) {
+        const int r = i & 127, s = (i >> 7) * 4 + w;
+        if (s >= steps) continue;
+        uint32_t v[2] = {0u, 0u};  // past the row's end: the smallest scale, on codes that are zero
+        if (r < rows) {
+            const uint8_t* p = src + static_cast<int64_t>(r) * nb + 8 * s;
+            if (ch.how == 8) {
+                const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+                v[0] = q.x, v[1] = q.y;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (8 * s + j < nb) v[j >> 2] |= static_cast<uint32_t>(__ldg(p + j)) << (8 * (j & 3));
+            }
+        }
+        uint32_t* to = reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(s) * mxp::kChunk + 16 * (r & 31) +
+                                                   4 * (r >> 5));
+        to[0] = v[0];
+        to[128] = v[1];
+    }
+}
+
 int mx_gemm_tile_rows(int64_t R, int n) { return R <= 32 * static_cast<int64_t>(n) ? 32 : 128; }
+
+bool mx_gemm_uses_pairs(const MxGemmArgs& a, int num_sms) {
+    const int64_t cols = a.b2_codes ? 128 : 256;
+    return a.R >= 256 * static_cast<int64_t>(a.n) && (a.R / 256) * ((a.N + cols - 1) / cols) >= num_sms / 2;
+}
+
+MxChunks mx_gemm_chunks(const MxGemmArgs& a) {
+    MxChunks ch{};
+    ch.steps = (a.K + kBK - 1) / kBK;
+    ch.a_blocks = static_cast<int>(2 * ((a.R + mxp::kTileRows - 1) / mxp::kTileRows + a.n));
+    ch.col_blocks = (a.N + 127) / 128;
+    ch.blocks = ch.a_blocks + static_cast<int64_t>(a.n) * ch.col_blocks * (a.b2_codes ? 2 : 1);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.a_scales) | reinterpret_cast<uintptr_t>(a.b_scales) |
+                         reinterpret_cast<uintptr_t>(a.b2_scales) | static_cast<uintptr_t>(a.K / 32);
+    ch.how = at % 8 == 0 ? 8 : 1;
+    return ch;
+}
+
+template <bool kPair, bool kBf16Out>
+static cudaError_t launch_pairs(const CUtensorMap* m, const MxGemmArgs& a, const MxChunks& ch, int num_sms,
+                                cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(mx_gemm_pair_kernel<kPair, kBf16Out>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, mxp::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms / 2 * 2));
+    cfg.blockDim = dim3(mxp::kThreads);
+    cfg.dynamicSmemBytes = mxp::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = (g_chain_started && pdl_enabled()) ? 2 : 1;
+    g_chain_started = true;
+    return cudaLaunchKernelEx(&cfg, mx_gemm_pair_kernel<kPair, kBf16Out>, m[0], m[1], m[2], m[3], m[4], a, ch,
+                              a.N % (kBf16Out ? 8 : 4) == 0 ? 1 : 0);
+}
+
+cudaError_t launch_mx_gemm_pairs(const CUtensorMap* m, const MxGemmArgs& a, bool bf16_out, const MxChunks& ch,
+                                 int num_sms, cudaStream_t st) {
+    cudaError_t e = launch_k(mx_scales_kernel, dim3(static_cast<unsigned>(ch.blocks)), dim3(256), 0, st, a, ch);
+    if (e != cudaSuccess) return e;
+    if (a.b2_codes)
+        return bf16_out ? launch_pairs<true, true>(m, a, ch, num_sms, st)
+                        : launch_pairs<true, false>(m, a, ch, num_sms, st);
+    return bf16_out ? launch_pairs<false, true>(m, a, ch, num_sms, st)
+                    : launch_pairs<false, false>(m, a, ch, num_sms, st);
+}
 
 template <bool kPair, bool kBf16Out, int kBN, int kTM>
 static cudaError_t launch(const CUtensorMap* m, const MxGemmArgs& a, int num_sms, cudaStream_t st) {

@@ -24,6 +24,8 @@ struct FfnWorkspace {
     void* da = nullptr;        // [grad_rows][F]
     void* db = nullptr;
     int64_t grad_rows = 0;
+    void* chunks = nullptr;    // scales of the MXFP4 product, turned over
+    int64_t chunk_bytes = 0;
     std::vector<void*> allocations;
 };
 
@@ -45,7 +47,15 @@ moe_status open_handle(moe_handle* h, HandleView* v);
 // outwards, strides of the axes after the first in bytes.
 bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                  const uint32_t* box);
-// The same for bytes.
+// The same with 64-byte swizzle, for bf16 and fp32.
+bool encode_bf16_64(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box);
+bool encode_f32_64(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                   const uint32_t* box);
+// Unswizzled, for 32-bit words.
+bool encode_words(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                  const uint32_t* box);
+// 128-byte swizzle, for bytes.
 bool encode_bytes(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                   const uint32_t* box);
 moe_status failed(moe_status s, const char* fmt, ...);  // sets moe_last_error()

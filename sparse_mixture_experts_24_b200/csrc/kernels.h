@@ -410,8 +410,13 @@ cudaError_t launch_ffn_maps(const CUtensorMap* maps5, const int32_t* offsets, in
 // launch_ffn_tc is to be taken.  The weights' maps are the same.
 int ffn_few_rows(int op, const FfnArgs& f);
 cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, int num_sms, cudaStream_t st);
-cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnArgs& f, const void* dw_maps, int num_sms,
-                          cudaStream_t st);
+// Output maps in 32 x 32 boxes with 64-byte swizzle: kFfnUp h, gate, up; kFfnDown
+// y; kFfnGrad da, db, h; kFfnDx dx; kFfnDw dw1, dw3, dw2 (3-D: column, row, expert).
+struct FfnOutMaps {
+    CUtensorMap m[3];
+};
+cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnOutMaps& out, const FfnArgs& f,
+                          const void* dw_maps, int num_sms, cudaStream_t st);
 
 // MXFP4 (mxfp4.cu): codes [..][K/2] and E8M0 scales [..][K/32], blocks of 32
 // along K; values (the type of the source), if given, receives what they stand
@@ -436,6 +441,22 @@ struct MxGemmArgs {
 // maps: A codes [R][K/2] in boxes of 128 bytes x mx_gemm_tile_rows rows, W and
 // the pair's codes [n][N][K/2] in boxes of 128 bytes x 128 rows.
 int mx_gemm_tile_rows(int64_t R, int n);
+// For many rows per expert (mx_gemm_uses_pairs), on CTA pairs, with the scales
+// turned over first into ch.base (ch.blocks * ch.steps KB of scratch); maps[3]:
+// out in boxes of 32 rows x 64 bytes with 64-byte swizzle, unused where a row
+// of out is no multiple of 16 bytes; maps[4]: ch.base as 32-bit words
+// [ch.blocks * ch.steps][256], a row per box.  Two launches.
+struct MxChunks {
+    uint8_t* base;
+    int64_t blocks;  // of 128 rows of A, then of 128 columns of W, then of P
+    int steps;       // 1 KB each
+    int a_blocks, col_blocks;
+    int how;         // 8: the scales' rows are 8-byte aligned and a multiple of 8 long; 1: byte by byte
+};
+bool mx_gemm_uses_pairs(const MxGemmArgs& a, int num_sms);
+MxChunks mx_gemm_chunks(const MxGemmArgs& a);
+cudaError_t launch_mx_gemm_pairs(const CUtensorMap* maps, const MxGemmArgs& a, bool bf16_out, const MxChunks& ch,
+                                 int num_sms, cudaStream_t st);
 cudaError_t launch_mx_gemm(const CUtensorMap* maps, const MxGemmArgs& a, bool bf16_out, int num_sms, cudaStream_t st);
 
 }  // namespace moe

@@ -339,7 +339,7 @@ moe_status check_device(moe_handle* h) {
 }  // namespace
 
 namespace moe_api_detail {
-static bool encode(CUtensorMapDataType type, CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+static bool encode(CUtensorMapDataType type, CUtensorMapSwizzle swizzle, CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                    const uint64_t* strides, const uint32_t* box) {
     EncodeTiledFn f = encode_fn();
     if (!f) return false;
@@ -352,16 +352,28 @@ static bool encode(CUtensorMapDataType type, CUtensorMap* m, const void* base, i
         if (i + 1 < rank) s[i] = strides[i];
     }
     return f(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 bool encode_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                  const uint32_t* box) {
-    return encode(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, m, base, rank, dims, strides, box);
+    return encode(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, m, base, rank, dims, strides, box);
+}
+bool encode_bf16_64(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box) {
+    return encode(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_64B, m, base, rank, dims, strides, box);
+}
+bool encode_f32_64(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                   const uint32_t* box) {
+    return encode(CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_64B, m, base, rank, dims, strides, box);
+}
+bool encode_words(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                  const uint32_t* box) {
+    return encode(CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, m, base, rank, dims, strides, box);
 }
 bool encode_bytes(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                   const uint32_t* box) {
-    return encode(CU_TENSOR_MAP_DATA_TYPE_UINT8, m, base, rank, dims, strides, box);
+    return encode(CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, m, base, rank, dims, strides, box);
 }
 
 moe_status open_handle(moe_handle* h, HandleView* v) {

@@ -102,6 +102,10 @@ PRODUCTS = [
     (2, [0, 300, 300], 300, 1000, 768),
     # more tiles than SMs, and scale rows that are not whole words
     (4, [0, 500, 500, 777, 1201], 1201, 4104, 1184),
+    # many rows per expert: CTA pairs, ragged ends, columns that are no whole vectors
+    (1, None, 1300, 5000, 480),
+    (3, [5, 300, 300, 1103], 1110, 4999, 320),
+    (2, [0, 1000, 2051], 2051, 4608, 2080),
 ]
 
 
