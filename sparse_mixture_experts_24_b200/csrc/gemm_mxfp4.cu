@@ -768,6 +768,7 @@ __global__ void __launch_bounds__(mxp::kThreads, 1)
 // of W, then of P.
 __global__ void __launch_bounds__(256) mx_scales_kernel(const MxGemmArgs args, const MxChunks ch) {
     __shared__ SegmentPlan plan;
+    __shared__ uint32_t slab[128][33];
     griddep_wait();
     load_plan(plan, args.offsets, args.n, args.R, mxp::kTileRows, args.status);
     griddep_launch_dependents();
@@ -794,28 +795,36 @@ __global__ void __launch_bounds__(256) mx_scales_kernel(const MxGemmArgs args, c
         rows = static_cast<int>(min(static_cast<int64_t>(128), args.N - col));
         src = (second ? args.b2_scales : args.b_scales) + (e * args.N + col) * nb;
     }
-    // four neighbouring lanes read 32 bytes of one row together (four steps), and
-    // a warp eight rows
-    const int w = threadIdx.x & 3;
-    for (int i = threadIdx.x >> 2; i < 128 * ((steps + 3) / 4); i += 64) {
-        const int r = i & 127, s = (i >> 7) * 4 + w;
-        if (s >= steps) continue;
-        uint32_t v[2] = {0u, 0u};  // past the row's end: the smallest scale, on codes that are zero
-        if (r < rows) {
-            const uint8_t* p = src + static_cast<int64_t>(r) * nb + 8 * s;
-            if (ch.how == 8) {
-                const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
-                v[0] = q.x, v[1] = q.y;
-            } else {
+    // Slabs of 16 steps through shared memory: a warp reads one row's 128 bytes and
+    // writes 512 contiguous ones.
+    for (int s0 = 0; s0 < steps; s0 += 16) {
+        const int n_steps = min(16, steps - s0), have = nb - 8 * s0;
+        uint32_t v[16];  // all in flight together; past the row's end the smallest scale
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (8 * s + j < nb) v[j >> 2] |= static_cast<uint32_t>(__ldg(p + j)) << (8 * (j & 3));
+        for (int j = 0; j < 16; ++j) {
+            const int r = (threadIdx.x >> 5) + 8 * j, q = threadIdx.x & 31;
+            const uint8_t* p = src + static_cast<int64_t>(r) * nb + 8 * s0 + 4 * q;
+            v[j] = 0u;
+            if (r < rows && 4 * q < have) {
+                if (ch.words) {
+                    v[j] = __ldg(reinterpret_cast<const uint32_t*>(p));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (4 * q + i < have) v[j] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * i);
+                }
             }
         }
-        uint32_t* to = reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(s) * mxp::kChunk + 16 * (r & 31) +
-                                                   4 * (r >> 5));
-        to[0] = v[0];
-        to[128] = v[1];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) slab[(threadIdx.x >> 5) + 8 * j][threadIdx.x & 31] = v[j];
+        __syncthreads();
+        // 16 bytes: rows i, i + 32, i + 64, i + 96 of one word
+        for (int u = threadIdx.x; u < n_steps * 64; u += 256) {
+            const int i = u & 31, q = u >> 5;
+            reinterpret_cast<uint4*>(dst + static_cast<int64_t>(s0) * mxp::kChunk)[u] =
+                make_uint4(slab[i][q], slab[i + 32][q], slab[i + 64][q], slab[i + 96][q]);
+        }
+        __syncthreads();
     }
 }
 
@@ -834,7 +843,7 @@ MxChunks mx_gemm_chunks(const MxGemmArgs& a) {
     ch.blocks = ch.a_blocks + static_cast<int64_t>(a.n) * ch.col_blocks * (a.b2_codes ? 2 : 1);
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.a_scales) | reinterpret_cast<uintptr_t>(a.b_scales) |
                          reinterpret_cast<uintptr_t>(a.b2_scales) | static_cast<uintptr_t>(a.K / 32);
-    ch.how = at % 8 == 0 ? 8 : 1;
+    ch.words = at % 4 == 0 ? 1 : 0;
     return ch;
 }
 

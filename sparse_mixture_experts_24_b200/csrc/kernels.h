@@ -451,7 +451,7 @@ struct MxChunks {
     int64_t blocks;  // of 128 rows of A, then of 128 columns of W, then of P
     int steps;       // 1 KB each
     int a_blocks, col_blocks;
-    int how;         // 8: the scales' rows are 8-byte aligned and a multiple of 8 long; 1: byte by byte
+    int words;       // the scales' rows are whole 4-byte words at 4-byte addresses
 };
 bool mx_gemm_uses_pairs(const MxGemmArgs& a, int num_sms);
 MxChunks mx_gemm_chunks(const MxGemmArgs& a);
