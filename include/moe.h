@@ -536,8 +536,7 @@ MOE_API moe_status moe_ep_buffer_close(void *ptr, int opened);
  * valid.  Calls on one handle share it: order them, graph replays included.
  *
  * moe_reserve_ffn: room for R_max rows, for the forward pass (backward = 0) or
- * both (backward = 1); moe_matmul_mxfp4 needs it only before a capture (R_max
- * = 1 serves).
+ * both (backward = 1).
  *   Errors: MOE_ERR_INVALID_ARG (null handle, R_max outside [0, 2^31 - 257],
  *   backward not 0 or 1, another device), MOE_ERR_UNSUPPORTED, MOE_ERR_ALLOC.
  */
@@ -608,12 +607,17 @@ MOE_API moe_status moe_quantize_weights_mxfp4(int n, int rows, int cols, const v
  * out [R][N] in the handle's dtype, rounded once from fp32 accumulators.  N and
  * K are free (the handle's d, ffn and K are not used).  Rows outside the
  * segments are not touched; bad offsets as for moe_ffn_forward.  Row and
- * matrix scales of 255 give NaN.
+ * matrix scales of 255 give NaN.  The call turns the scales over into scratch of
+ * the handle (a 16th to an 8th of the codes' bytes), which grows on demand as the
+ * workspace above does; moe_reserve_matmul_mxfp4 makes room for calls of up to
+ * R_max rows (pair = 1: with a second matrix), needed before a capture unless an
+ * earlier call of the size has been made.
  *   Errors: MOE_ERR_INVALID_ARG (R as above, N outside [1, 2^20], K not a
  *   multiple of 32 in [32, 2^20], null / misaligned pointer, one of the pair's
  *   null, offsets NULL with n > 1, another device), MOE_ERR_UNSUPPORTED,
  *   MOE_ERR_ALLOC, MOE_ERR_CUDA.
  */
+MOE_API moe_status moe_reserve_matmul_mxfp4(moe_handle *h, int64_t R_max, int N, int K, int pair);
 MOE_API moe_status moe_matmul_mxfp4(moe_handle *h, int64_t R, int N, int K, const int32_t *offsets,
                                     const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *w_codes,
                                     const uint8_t *w_scales, const uint8_t *pair_codes,

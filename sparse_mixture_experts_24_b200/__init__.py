@@ -83,6 +83,7 @@ lib.moe_ffn_forward.argtypes = [_vp, _i64] + [_vp] * 9
 lib.moe_ffn_backward.argtypes = [_vp, _i64] + [_vp] * 13
 lib.moe_quantize_mxfp4.argtypes = [_i64, _int, _vp, _int, _vp, _vp, _vp, _vp]
 lib.moe_quantize_weights_mxfp4.argtypes = [_int, _int, _int, _vp, _int, _vp, _vp, _vp, _vp]
+lib.moe_reserve_matmul_mxfp4.argtypes = [_vp, _i64, _int, _int, _int]
 lib.moe_matmul_mxfp4.argtypes = [_vp, _i64, _int, _int] + [_vp] * 9
 lib.moe_last_error.restype = ctypes.c_char_p
 lib.moe_version.restype = ctypes.c_char_p
@@ -94,7 +95,8 @@ for _f in ("moe_create", "moe_reserve", "moe_forward", "moe_route", "moe_dispatc
            "moe_quantize_weights_fp4", "moe_forward_fp4", "moe_pack_weights_w4a4", "moe_forward_w4a4",
            "moe_pack_weights_w4a16", "moe_forward_w4a16", "moe_ep_dispatch", "moe_ep_experts", "moe_ep_combine", "moe_ep_buffer_alloc", "moe_ep_buffer_open",
            "moe_ep_buffer_close", "moe_set_gate_rounding", "moe_reserve_ffn", "moe_ffn_forward",
-           "moe_ffn_backward", "moe_quantize_mxfp4", "moe_quantize_weights_mxfp4", "moe_matmul_mxfp4"):
+           "moe_ffn_backward", "moe_quantize_mxfp4", "moe_quantize_weights_mxfp4", "moe_matmul_mxfp4",
+           "moe_reserve_matmul_mxfp4"):
     getattr(lib, _f).restype = _int
 
 EXPORTED = ("moe_create", "moe_reserve", "moe_forward", "moe_route", "moe_dispatch",
@@ -107,7 +109,7 @@ EXPORTED = ("moe_create", "moe_reserve", "moe_forward", "moe_route", "moe_dispat
             "moe_ep_dispatch", "moe_ep_experts", "moe_ep_combine",
             "moe_ep_buffer_alloc", "moe_ep_buffer_open", "moe_ep_buffer_close", "moe_set_gate_rounding",
             "moe_reserve_ffn", "moe_ffn_forward", "moe_ffn_backward", "moe_quantize_mxfp4",
-            "moe_quantize_weights_mxfp4", "moe_matmul_mxfp4")
+            "moe_quantize_weights_mxfp4", "moe_matmul_mxfp4", "moe_reserve_matmul_mxfp4")
 
 TRACE_STAGES = ("router", "dispatch", "gather", "gemm1", "gemm2", "combine")
 
@@ -417,6 +419,10 @@ def moe_quantize_weights_mxfp4(n, rows, cols, w, dtype, codes, scales, values=No
                                           _stream(stream)), "moe_quantize_weights_mxfp4")
 
 
+def moe_reserve_matmul_mxfp4(h, R_max: int, N: int, K: int, pair: int) -> None:
+    _check(lib.moe_reserve_matmul_mxfp4(h, R_max, N, K, pair), "moe_reserve_matmul_mxfp4")
+
+
 def moe_matmul_mxfp4(h, R, N, K, offsets, a_codes, a_scales, w_codes, w_scales, pair_codes, pair_scales, out,
                      stream=None) -> None:
     _check(lib.moe_matmul_mxfp4(h, R, N, K, _ptr(offsets), _ptr(a_codes), _ptr(a_scales), _ptr(w_codes),
@@ -432,9 +438,12 @@ def _take(where: str, name: str, t, dtype, shape):
     """Refuse a tensor that the C ABI would misread: `t` has to be a contiguous
     CUDA tensor of this type and shape on the current device."""
     import torch
-    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()
-            and t.get_device() == torch.cuda.current_device()):
-        return
+    try:  # the common case first
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda
+                and t.get_device() == torch.cuda.current_device()):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _refuse(where, "%s is not a CUDA tensor" % name)
     if t.dtype != dtype:
@@ -701,6 +710,10 @@ class MoELayer:
             dw = [torch.empty_like(w) if need_dw else None for w in (w1, w3, w2)]
         moe_ffn_backward(self.h, R, offsets, x, w1, w3, w2, gate, up, dy, dx, *dw, _call_stream(stream))
         return (dx, *dw)
+
+    def reserve_matmul_mxfp4(self, R_max: int, N: int, K: int, pair: bool = False) -> None:
+        """Scratch of matmul_mxfp4 for up to R_max rows."""
+        moe_reserve_matmul_mxfp4(self.h, R_max, N, K, 1 if pair else 0)
 
     def matmul_mxfp4(self, a, w, pair=None, offsets=None, out=None, stream=None):
         """Grouped product of MXFP4 rows with the MXFP4 matrices of their expert

@@ -56,7 +56,7 @@ moe_status allocate(moe::FfnWorkspace* w, size_t bytes, cudaStream_t st, bool us
         if (cap != cudaStreamCaptureStatusNone)
             return failed(MOE_ERR_INVALID_ARG,
                           "the workspace is too small and cannot grow while the stream is captured: call "
-                          "moe_reserve_ffn first");
+                          "moe_reserve_ffn or moe_reserve_matmul_mxfp4 first");
     }
     void* p = nullptr;
     cudaError_t e = cudaMalloc(&p, bytes);
@@ -98,6 +98,15 @@ moe_status need(const HandleView& v, int64_t rows, bool backward, cudaStream_t s
         w->grad_rows = rows;
     }
     return MOE_OK;
+}
+
+// Scratch for `chunks` KB of scales of the MXFP4 product.
+moe_status need_chunks(const HandleView& v, int64_t chunks, cudaStream_t st, bool use_stream) {
+    moe::FfnWorkspace* w = v.ffn;
+    if (chunks * 1024 <= w->chunk_bytes) return MOE_OK;
+    moe_status s = allocate(w, static_cast<size_t>(chunks) * 1024, st, use_stream, &w->chunks);
+    if (s == MOE_OK) w->chunk_bytes = chunks * 1024;
+    return s;
 }
 
 moe::FfnArgs ffn_args(const HandleView& v, int64_t R, const int32_t* offsets) {
@@ -339,6 +348,14 @@ moe_status moe_ffn_backward(moe_handle* h, int64_t R, const int32_t* offsets, co
 }
 
 namespace {
+// N and K of the MXFP4 product.
+moe_status check_mx_shape(int N, int K) {
+    if (N < 1 || N > 1048576) return failed(MOE_ERR_INVALID_ARG, "N = %d outside [1, 1048576]", N);
+    if (K < 32 || K % 32 != 0 || K > 1048576)
+        return failed(MOE_ERR_INVALID_ARG, "K = %d is not a multiple of 32 in [32, 1048576]", K);
+    return MOE_OK;
+}
+
 // SM count of the current device; what a device is never changes, so it is
 // asked for once per device.
 moe_status device_of_call(int* sms) {
@@ -402,15 +419,31 @@ moe_status moe_quantize_weights_mxfp4(int n, int rows, int cols, const void* w, 
     return done();
 }
 
+moe_status moe_reserve_matmul_mxfp4(moe_handle* h, int64_t R_max, int N, int K, int pair) {
+    if (!h) return failed(MOE_ERR_INVALID_ARG, "null handle");
+    moe_status s = check_rows(R_max, "R_max");
+    if (s != MOE_OK) return s;
+    s = check_mx_shape(N, K);
+    if (s != MOE_OK) return s;
+    if (pair != 0 && pair != 1) return failed(MOE_ERR_INVALID_ARG, "pair = %d is neither 0 nor 1", pair);
+    if (R_max == 0) return done();
+    HandleView v;
+    s = open_handle(h, &v);
+    if (s != MOE_OK) return s;
+    s = need(v, 0, false, nullptr, false);
+    if (s != MOE_OK) return s;
+    s = need_chunks(v, moe::mx_gemm_most_chunks(R_max, v.n, N, K, pair), nullptr, false);
+    return s == MOE_OK ? done() : s;
+}
+
 moe_status moe_matmul_mxfp4(moe_handle* h, int64_t R, int N, int K, const int32_t* offsets, const uint8_t* a_codes,
                             const uint8_t* a_scales, const uint8_t* w_codes, const uint8_t* w_scales,
                             const uint8_t* pair_codes, const uint8_t* pair_scales, void* out, moe_stream_t stream) {
     if (!h) return failed(MOE_ERR_INVALID_ARG, "null handle");
     moe_status s = check_rows(R);
     if (s != MOE_OK) return s;
-    if (N < 1 || N > 1048576) return failed(MOE_ERR_INVALID_ARG, "N = %d outside [1, 1048576]", N);
-    if (K < 32 || K % 32 != 0 || K > 1048576)
-        return failed(MOE_ERR_INVALID_ARG, "K = %d is not a multiple of 32 in [32, 1048576]", K);
+    s = check_mx_shape(N, K);
+    if (s != MOE_OK) return s;
     if ((pair_codes == nullptr) != (pair_scales == nullptr))
         return failed(MOE_ERR_INVALID_ARG, "pair_codes and pair_scales must both be given or both be null");
     if (R == 0) return done();
@@ -430,57 +463,33 @@ moe_status moe_matmul_mxfp4(moe_handle* h, int64_t R, int N, int K, const int32_
     if (s != MOE_OK) return s;
     moe::MxGemmArgs a{offsets,  v.n,      R,          N,           K,   a_codes,      a_scales,
                       w_codes,  w_scales, pair_codes, pair_scales, out, v.ffn->status};
+    moe::MxChunks ch = moe::mx_gemm_chunks(a, v.num_sms);
+    s = need_chunks(v, ch.blocks * ch.steps, st, true);
+    if (s != MOE_OK) return s;
+    ch.base = static_cast<uint8_t*>(v.ffn->chunks);
     const uint64_t k2 = static_cast<uint64_t>(K) / 2, cols = static_cast<uint64_t>(N);
     const uint64_t a_dims[2] = {k2, static_cast<uint64_t>(R)}, a_strides[1] = {k2};
-    const uint32_t a_box[2] = {128, static_cast<uint32_t>(moe::mx_gemm_tile_rows(R, v.n))};
+    const uint32_t a_box[2] = {128, ch.tile_rows < 128 ? static_cast<uint32_t>(ch.tile_rows) : 128u};
     const uint64_t w_dims[3] = {k2, cols, static_cast<uint64_t>(v.n)}, w_strides[2] = {k2, k2 * cols};
     const uint32_t w_box[3] = {128, 128, 1};
-    CUtensorMap m[5] = {};
-    // out in boxes of 32 rows x 64 bytes, where its rows allow a map
-    const int per16 = v.bf16 ? 8 : 4;
     const uint64_t o_dims[2] = {cols, static_cast<uint64_t>(R)}, o_strides[1] = {cols * (v.bf16 ? 2 : 4)};
     const uint32_t o_box[2] = {v.bf16 ? 32u : 16u, 32};
-    if (N % per16 == 0 && !(v.bf16 ? moe_api_detail::encode_bf16_64(&m[3], out, 2, o_dims, o_strides, o_box)
-                                   : moe_api_detail::encode_f32_64(&m[3], out, 2, o_dims, o_strides, o_box)))
-        return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (MXFP4 product)");
-    if (!moe_api_detail::encode_bytes(&m[0], a_codes, 2, a_dims, a_strides, a_box) ||
-        !moe_api_detail::encode_bytes(&m[1], w_codes, 3, w_dims, w_strides, w_box) ||
-        (pair_codes && !moe_api_detail::encode_bytes(&m[2], pair_codes, 3, w_dims, w_strides, w_box)))
-        return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (MXFP4 product)");
-    // Pairs need scratch for the scales.  Where it cannot be had because the stream
-    // is captured, the other kernel takes the call: the same products in the same
-    // order.
-    bool pairs = moe::mx_gemm_uses_pairs(a, v.num_sms);
-    moe::MxChunks ch{};
-    if (pairs) {
-        ch = moe::mx_gemm_chunks(a);
-        const int64_t rows = ch.blocks * ch.steps;
-        if (rows * 1024 > v.ffn->chunk_bytes) {
-            cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-            cudaError_t e = cudaStreamIsCapturing(st, &cap);
-            if (e != cudaSuccess) {
-                cudaGetLastError();
-                return cuda_failed(e, "cudaStreamIsCapturing");
-            }
-            if (cap != cudaStreamCaptureStatusNone) {
-                pairs = false;
-            } else {
-                s = allocate(v.ffn, static_cast<size_t>(rows) * 1024, st, true, &v.ffn->chunks);
-                if (s != MOE_OK) return s;
-                v.ffn->chunk_bytes = rows * 1024;
-            }
-        }
-        ch.base = static_cast<uint8_t*>(v.ffn->chunks);
-        const uint64_t c_dims[2] = {256, static_cast<uint64_t>(rows)}, c_strides[1] = {1024};
-        const uint32_t c_box[2] = {256, 1};
-        if (pairs && !moe_api_detail::encode_words(&m[4], ch.base, 2, c_dims, c_strides, c_box))
-            return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (MXFP4 scales)");
-    }
+    const uint64_t c_dims[2] = {256, static_cast<uint64_t>(ch.blocks * ch.steps)}, c_strides[1] = {1024};
+    const uint32_t c_box[2] = {256, 1};
+    CUtensorMap m[5] = {};
+    using namespace moe_api_detail;
+    bool mapped = encode_bytes(&m[0], a_codes, 2, a_dims, a_strides, a_box) &&
+                  encode_bytes(&m[1], w_codes, 3, w_dims, w_strides, w_box) &&
+                  encode_words(&m[4], ch.base, 2, c_dims, c_strides, c_box);
+    if (pair_codes) mapped = mapped && encode_bytes(&m[2], pair_codes, 3, w_dims, w_strides, w_box);
+    if (ch.tile_rows > 128 && N % (v.bf16 ? 8 : 4) == 0)
+        mapped = mapped && (v.bf16 ? encode_bf16_64(&m[3], out, 2, o_dims, o_strides, o_box)
+                                   : encode_f32_64(&m[3], out, 2, o_dims, o_strides, o_box));
+    if (!mapped) return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (MXFP4 product)");
     moe::chain_begin();
-    cudaError_t e = pairs ? moe::launch_mx_gemm_pairs(m, a, v.bf16, ch, v.num_sms, st)
-                          : moe::launch_mx_gemm(m, a, v.bf16, v.num_sms, st);
+    cudaError_t e = moe::launch_mx_gemm(m, a, v.bf16, ch, v.num_sms, st);
     if (e != cudaSuccess) return cuda_failed(e, "MXFP4 product launch");
-    *v.launches += pairs ? 2 : 1;
+    *v.launches += 2;
     return done();
 }
 

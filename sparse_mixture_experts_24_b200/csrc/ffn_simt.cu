@@ -247,19 +247,18 @@ __global__ void __launch_bounds__(kThreads, kOp == kFfnGrad || kOp == kFfnDx ? 4
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (i % splits != rank) continue;
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            for (int q = 0; q < splits; ++q) {
+                const uint32_t from = mapa_shared(mine + i * 8 * kThreads * 4, q);
+                float u[8];  // eight loads in flight
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float v = 0.f;
-                for (int q = 0; q < splits; ++q) {
-                    float u;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(u)
-                                 : "r"(mapa_shared(mine + (i * 8 + j) * kThreads * 4, q))
-                                 : "memory");
-                    v += u;
-                }
-                acc[i][j] = v;
+                for (int j = 0; j < 8; ++j)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u[j]) : "r"(from + j * kThreads * 4) : "memory");
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += u[j];
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][j] = v[j];
         }
         cluster_sync();  // the partial sums stay until every block has read them
     }

@@ -6,25 +6,35 @@
 // (mxfp4.cu).  tcgen05.mma kind::mxf4 multiplies the E2M1 codes with their
 // power-of-two scales (one per 32 of K) and accumulates in fp32.
 //
-// One persistent CTA per SM, 384 threads, tiles of kTM rows x kBN columns (a
-// pair: 128 columns of W beside the same 128 of P), K in steps of 256:
+// Three kernels:
+//   mx_scales_kernel     turns the scales over.  The format keeps a row's scales
+//                        contiguous; the tensor core takes, per 128 rows and 128 of
+//                        K, 512 bytes with row r's four at 16 (r % 32) + 4 (r / 32).
+//                        It writes them as chunks of 1 KB per 128 rows (or columns)
+//                        and step into scratch, a 17th of the codes' bytes.  Turned
+//                        over by warps of the product kernel instead, from the rows 8
+//                        to 16 bytes at a time, they bound it: 8,192 rows over 8
+//                        experts, 4,096 x 14,336 twice, 597 to 1,641 us by five ways
+//                        of fetching them against 401 + 20 us.
+//   mx_gemm_kernel       one CTA per SM, tiles of kTM rows x kBN columns
+//   mx_gemm_pair_kernel  CTA pairs, 256 x 256 tiles, for many rows per expert
+//
+// mx_gemm_kernel, 352 threads, K in steps of 256 (a pair's tile: 128 columns of W
+// beside the same 128 of P):
 //   warp 0       TMA: codes of the tile's rows and columns (128 bytes per row and
-//                step, 128-byte swizzle; past K, N or R the copy reads zeros);
-//   warps 10-11  scales.  The format keeps a row's scales contiguous, the tensor
-//                core wants, per 128 rows and 128 of K, 512 bytes with row r's
-//                four at 16 (r % 32) + 4 (r / 32): these warps fetch 16 scales (two
-//                steps) of each row at a time, one fetch ahead, and turn them
-//                over on the way into shared memory, so no packed copy of the
-//                scales has to exist anywhere;
-//   warp 1       one thread copies a step's scales into tensor memory
-//                (tcgen05.cp 32x128b.warpx4) and issues its four MMAs (K 64);
-//                a copy holds the scales of two MMAs, told apart by the
-//                descriptor's scale id;
+//                step, 128-byte swizzle; past K, N or R the copy reads zeros) and
+//                their scale chunks;
+//   warp 10      one thread copies a step's scales into tensor memory (tcgen05.cp
+//                32x128b.warpx4); a copy holds the scales of two MMAs, told apart
+//                by the descriptor's scale id;
+//   warp 1       one thread issues the step's four MMAs (M 128, K 64);
 //   warps 2-9    epilogue, two per 32 accumulator rows, each on half the columns:
 //                the accumulators go to registers and are handed back first.
-// kTM = 32 loads only 32 rows of A per tile (batches of few rows per expert);
-// the MMA's other 96 rows read whatever follows and are never stored.
+// kTM = 64 loads only 64 rows of A per tile (batches of few rows per expert); the
+// MMA's other 64 rows read whatever follows and are never stored.
 // Every wait is bounded (common.cuh).
+#include <algorithm>
+
 #include "ffn.cuh"
 #include "kernels.h"
 
@@ -37,40 +47,43 @@ constexpr int kBBlockBytes = 128 * 128;     // 128 columns
 constexpr int kSfBytes = 2 * 512;           // a step's scales of 128 rows
 constexpr int kTmemCols = 512;
 constexpr int kEpiWarps = 8;
-constexpr int kLoadWarp = 2 + kEpiWarps, kLoadThreads = 64;
-constexpr int kThreads = kLoadWarp * 32 + kLoadThreads;
-constexpr int kMaxStages = 8;
+constexpr int kCopyWarp = 2 + kEpiWarps;
+constexpr int kThreads = (kCopyWarp + 1) * 32;
+constexpr int kMaxStages = 7;
+constexpr int kPairRows = 256;              // rows of a tile of mx_gemm_pair_kernel
 
 template <int kBN, int kTM>
 struct Cfg {
     static constexpr int kBlocks = kBN / 128;
     static constexpr int kABytes = kTM * 128;
     static constexpr int kCodeBytes = kABytes + kBlocks * kBBlockBytes;
-    static constexpr int kStageBytes = (kCodeBytes + (1 + kBlocks) * kSfBytes + 1023) / 1024 * 1024;
-    static constexpr int kStages = kBN == 128 ? (kTM == 32 ? 8 : 6) : (kTM == 32 ? 5 : 4);
+    static constexpr int kStageBytes = kCodeBytes + (1 + kBlocks) * kSfBytes;
+    static constexpr int kStages = kBN == 128 ? (kTM == 64 ? 7 : 6) : 4;
     static constexpr int kAccBufs = kBN == 128 ? 2 : 1;
     static constexpr int kSfCols = 8 * (1 + kBlocks);  // per stage
     static constexpr int kSfBase = kAccBufs * kBN;
-    static constexpr int kRows = kTM + kBN;            // rows whose scales a step needs
-    static constexpr int kPer = (kRows + kLoadThreads - 1) / kLoadThreads;
     static_assert(kSfBase + kStages * kSfCols <= kTmemCols && kStages <= kMaxStages, "tensor memory");
+    static_assert(kStageBytes % 1024 == 0, "the codes' swizzle");
 };
 
 struct __align__(16) Tail {
     uint64_t full[kMaxStages];
     uint64_t empty[kMaxStages];
+    uint64_t scales[kMaxStages];  // in tensor memory
+    uint64_t copied;
     uint64_t accum_full[2];
     uint64_t accum_empty[2];
     uint64_t done;
     uint32_t tmem_base;
     SegmentPlan plan;
 };
+constexpr int kTailBytes = (static_cast<int>(sizeof(Tail)) + 1023) / 1024 * 1024;
 
-constexpr int kTailBytes = (static_cast<int>(sizeof(Tail)) + 127) / 128 * 128;
-
+// Shared memory, 1 KB aligned: barriers and plan, the ring, an exchange block per
+// epilogue warp.
 template <int kBN, int kTM>
 constexpr int smem_bytes() {
-    return Cfg<kBN, kTM>::kStages * Cfg<kBN, kTM>::kStageBytes + kTailBytes + kEpiWarps * kExchangeBytes + 1024;
+    return kTailBytes + Cfg<kBN, kTM>::kStages * Cfg<kBN, kTM>::kStageBytes + kEpiWarps * kExchangeBytes;
 }
 
 struct Tile {
@@ -123,25 +136,6 @@ __device__ __forceinline__ float silu(float a) {
     return __fdividef(a, 1.f + (kBf16Out ? __expf(-a) : expf(-a)));
 }
 
-// The 16 scales g * 16 .. of one row, zeros (the smallest scale, on codes that
-// are zero too) past the row's nb.  `how`: 4 -- rows are 16-byte aligned and a
-// multiple of 16 long; 2 -- the same for 4; else byte by byte.
-__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int g, int nb, int how) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    const int at = g * 16;
-    if (how == 4) return __ldg(reinterpret_cast<const uint4*>(row + at));
-    if (how == 2) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (at + 4 * i < nb) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + at + 4 * i));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (at + i < nb) w[i >> 2] |= static_cast<uint32_t>(__ldg(row + at + i)) << (8 * (i & 3));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Columns col .. col+31 of 32 rows of out (a lane its row, `valid` of them).
 // Rows that are whole vectors go through the warp's exchange block, others
 // element by element.
@@ -183,25 +177,26 @@ using namespace mxg;
 template <bool kPair, bool kBf16Out, int kBN, int kTM>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                   const __grid_constant__ CUtensorMap tm_b2, const MxGemmArgs args, const int scales_how) {
+                   const __grid_constant__ CUtensorMap tm_b2, const __grid_constant__ CUtensorMap tm_chunks,
+                   const MxGemmArgs args, const MxChunks ch) {
     using C = Cfg<kBN, kTM>;
     static_assert(!kPair || kBN == 256, "a pair's tile is one block of each matrix");
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~static_cast<uintptr_t>(1023));
-    Tail* tail = reinterpret_cast<Tail*>(smem + C::kStages * C::kStageBytes);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Tail* tail = reinterpret_cast<Tail*>(smem_raw);
+    uint8_t* smem = smem_raw + kTailBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kColsOut = kPair ? 128 : kBN;  // output columns of a tile
     const int n_tiles = (args.N + kColsOut - 1) / kColsOut;
-    const int steps = (args.K + kBK - 1) / kBK;
-    const int nb = args.K / 32;
+    const int steps = ch.steps;
     int* status = args.status;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(smem_u32(&tail->full[s]), 1 + kLoadThreads);
+            mbar_init(smem_u32(&tail->full[s]), 1);
             mbar_init(smem_u32(&tail->empty[s]), 1);
+            mbar_init(smem_u32(&tail->scales[s]), 1);
         }
+        mbar_init(smem_u32(&tail->copied), 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&tail->accum_full[b]), 1);
             mbar_init(smem_u32(&tail->accum_empty[b]), kEpiWarps);
@@ -213,13 +208,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&tm_a);
         tma_prefetch_desc(&tm_b);
+        tma_prefetch_desc(&tm_chunks);
         if (kPair) tma_prefetch_desc(&tm_b2);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(&tail->tmem_base), kTmemCols);
         tmem_relinquish();
     }
-    griddep_wait();
     load_plan(tail->plan, args.offsets, args.n, args.R, kTM, status);
     tc_fence_before();
     __syncthreads();
@@ -232,6 +227,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             // ---------------- TMA producer ----------------
+            auto codes = [&](const Tile& ti, int ks, int stage) {
+                const uint32_t fb = smem_u32(&tail->full[stage]);
+                mbar_arrive_expect_tx(fb, C::kStageBytes);
+                const uint32_t base = smem_u32(smem + stage * C::kStageBytes);
+                tma_load_2d(base, &tm_a, fb, ks * 128, ti.row0);
+#pragma unroll
+                for (int b = 0; b < C::kBlocks; ++b)
+                    tma_load_3d(base + C::kABytes + b * kBBlockBytes, kPair && b == 1 ? &tm_b2 : &tm_b, fb, ks * 128,
+                                kPair ? ti.n_tile * 128 : ti.n_tile * kBN + b * 128, ti.e);
+            };
+            // The ring's first codes do not depend on the kernel before, which turns the
+            // scales over: they are on their way while it runs.
+            const int ahead = first < total ? min(C::kStages, steps) : 0;
+            for (int ks = 0; ks < ahead; ++ks) codes(tile_at<kTM>(first, plan, args.n, n_tiles), ks, ks);
+            griddep_wait();
             int stage = 0;
             uint32_t phase = 0;
             int armed[kMaxStages];
@@ -239,20 +249,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = first; t < total && ok; t += stride) {
                 const Tile ti = tile_at<kTM>(t, plan, args.n, n_tiles);
+                // chunks of the tile's rows, and of its blocks of 128 columns
+                const int sa = (plan.blk[ti.e] + (ti.row0 - plan.off[ti.e]) / kTM) * steps;
+                const int cols = ch.a_blocks + ti.e * ch.col_blocks;
+                const int c0 = kPair ? ti.n_tile : C::kBlocks * ti.n_tile;
                 for (int ks = 0; ks < steps; ++ks) {
-                    if (!mbar_wait(smem_u32(&tail->empty[stage]), phase ^ 1u, status, kStatusTimeoutEmpty)) {
-                        ok = false;
-                        break;
+                    if (t != first || ks >= ahead) {
+                        if (!mbar_wait(smem_u32(&tail->empty[stage]), phase ^ 1u, status, kStatusTimeoutEmpty)) {
+                            ok = false;
+                            break;
+                        }
+                        codes(ti, ks, stage);
                     }
-                    const uint32_t fb = smem_u32(&tail->full[stage]);
-                    mbar_arrive_expect_tx(fb, C::kCodeBytes);
                     armed[stage] = static_cast<int>(phase);
-                    const uint32_t base = smem_u32(smem + stage * C::kStageBytes);
-                    tma_load_2d(base, &tm_a, fb, ks * 128, ti.row0);
+                    const uint32_t fb = smem_u32(&tail->full[stage]);
+                    const uint32_t sf = smem_u32(smem + stage * C::kStageBytes) + C::kCodeBytes;
+                    tma_load_2d(sf, &tm_chunks, fb, 0, sa + ks);
 #pragma unroll
-                    for (int b = 0; b < C::kBlocks; ++b)
-                        tma_load_3d(base + C::kABytes + b * kBBlockBytes, kPair && b == 1 ? &tm_b2 : &tm_b, fb,
-                                    ks * 128, kPair ? ti.n_tile * 128 : ti.n_tile * kBN + b * 128, ti.e);
+                    for (int b = 0; b < C::kBlocks; ++b) {
+                        // a last, lone block of columns: the second one's outputs are not stored
+                        const int c = kPair ? c0 + b * args.n * ch.col_blocks : min(c0 + b, ch.col_blocks - 1);
+                        tma_load_2d(sf + (1 + b) * kSfBytes, &tm_chunks, fb, 0, (cols + c) * steps + ks);
+                    }
                     if (++stage == C::kStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -266,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            // ---------------- scale copies and MMAs ----------------
+            // ---------------- MMA issuer ----------------
             int stage = 0;
             uint32_t phase = 0;
             int local = 0;
@@ -281,23 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(buf * kBN);
                 for (int ks = 0; ks < steps; ++ks) {
-                    if (!mbar_wait(smem_u32(&tail->full[stage]), phase, status, kStatusTimeoutFull)) {
+                    // the stage's scales are in tensor memory, so its codes have landed too
+                    if (!mbar_wait(smem_u32(&tail->scales[stage]), phase, status, kStatusTimeoutFull)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t base = smem_u32(smem + stage * C::kStageBytes);
-                    const uint32_t sf_smem = base + C::kCodeBytes;
                     const uint32_t sf = tmem_base + static_cast<uint32_t>(C::kSfBase + stage * C::kSfCols);
-                    // tensor memory: A's two chunks, then for either chunk the blocks of B
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        tc_cp_32x128b_warpx4(sf + 4 * c, make_smem_desc(sf_smem + c * 512, 0, 128, 0));
-#pragma unroll
-                        for (int b = 0; b < C::kBlocks; ++b)
-                            tc_cp_32x128b_warpx4(sf + 8 + 4 * (c * C::kBlocks + b),
-                                                 make_smem_desc(sf_smem + (1 + b) * kSfBytes + c * 512, 0, 128, 0));
-                    }
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         const int c = kk >> 1;
@@ -314,80 +323,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (ok) tc_commit(smem_u32(&tail->accum_full[buf]));
             }
-            // every copy and MMA is done before tensor memory is freed
+            // every MMA is done before tensor memory is freed
             tc_commit(smem_u32(&tail->done));
             mbar_wait(smem_u32(&tail->done), 0, status, kStatusTimeoutDrain);
         }
-    } else if (warp >= kLoadWarp) {
-        // ---------------- scales ----------------
-        const int lt = static_cast<int>(threadIdx.x) - kLoadWarp * 32;
-        uint4 cur[C::kPer], next[C::kPer];
-        const int groups = (steps + 1) / 2;  // of two steps
-        auto fetch = [&](int t, int g, uint4 (&to)[C::kPer]) {
-            const Tile ti = tile_at<kTM>(t, plan, args.n, n_tiles);
-#pragma unroll
-            for (int i = 0; i < C::kPer; ++i) {
-                const int r = lt + i * kLoadThreads;
-                const uint8_t* row = nullptr;
-                if (r < kTM) {
-                    if (r < ti.rows) row = args.a_scales + (static_cast<int64_t>(ti.row0) + r) * nb;
-                } else if (r < C::kRows) {
-                    const int j = r - kTM, b = j >> 7;
-                    const int col = kPair ? ti.n_tile * 128 + (j & 127) : ti.n_tile * kBN + j;
-                    if (col < args.N)
-                        row = (kPair && b ? args.b2_scales : args.b_scales) +
-                              (static_cast<int64_t>(ti.e) * args.N + col) * nb;
-                }
-                to[i] = row ? load_scales(row, g, nb, scales_how) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        if (first < total) fetch(first, 0, next);
-        for (int t = first; t < total && ok; t += stride) {
-            for (int g = 0; g < groups && ok; ++g) {
-#pragma unroll
-                for (int i = 0; i < C::kPer; ++i) cur[i] = next[i];
-                if (g + 1 < groups)
-                    fetch(t, g + 1, next);
-                else if (t + stride < total)
-                    fetch(t + stride, 0, next);
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (2 * g + s >= steps) break;
-                    if (!mbar_wait(smem_u32(&tail->empty[stage]), phase ^ 1u, status, kStatusTimeoutEmpty)) {
+    } else if (warp == kCopyWarp) {
+        if (lane == 0) {
+            // ---------------- scales into tensor memory ----------------
+            // Tensor memory: A's two chunks, then for either chunk the blocks of B.  A
+            // stage's columns are written again only after its next full barrier, which
+            // follows the MMAs that read them.
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = first; t < total && ok; t += stride) {
+                for (int ks = 0; ks < steps; ++ks) {
+                    if (!mbar_wait(smem_u32(&tail->full[stage]), phase, status, kStatusTimeoutFull)) {
                         ok = false;
                         break;
                     }
-                    uint8_t* sf = smem + stage * C::kStageBytes + C::kCodeBytes;
+                    tc_fence_after();
+                    const uint32_t sf_smem = smem_u32(smem + stage * C::kStageBytes) + C::kCodeBytes;
+                    const uint32_t sf = tmem_base + static_cast<uint32_t>(C::kSfBase + stage * C::kSfCols);
 #pragma unroll
-                    for (int i = 0; i < C::kPer; ++i) {
-                        const int r = lt + i * kLoadThreads;
-                        if (r < C::kRows) {
-                            const int j = r < kTM ? r : (r - kTM) & 127;
-                            const int block = r < kTM ? 0 : 1 + ((r - kTM) >> 7);
-                            uint32_t* dst = reinterpret_cast<uint32_t*>(sf + block * kSfBytes + 16 * (j & 31) +
-                                                                        4 * (j >> 5));
-                            dst[0] = s == 0 ? cur[i].x : cur[i].z;
-                            dst[128] = s == 0 ? cur[i].y : cur[i].w;
-                        }
+                    for (int c = 0; c < 2; ++c) {
+                        tc_cp_32x128b_warpx4(sf + 4 * c, make_smem_desc(sf_smem + c * 512, 0, 128, 0));
+#pragma unroll
+                        for (int b = 0; b < C::kBlocks; ++b)
+                            tc_cp_32x128b_warpx4(sf + 8 + 4 * (c * C::kBlocks + b),
+                                                 make_smem_desc(sf_smem + (1 + b) * kSfBytes + c * 512, 0, 128, 0));
                     }
-                    fence_proxy_async_smem();
-                    mbar_arrive(smem_u32(&tail->full[stage]));
+                    tc_commit(smem_u32(&tail->scales[stage]));
                     if (++stage == C::kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
+            tc_commit(smem_u32(&tail->copied));
+            mbar_wait(smem_u32(&tail->copied), 0, status, kStatusTimeoutDrain);
         }
     } else {
         // ---------------- epilogue (warps 2..9) ----------------
         const int quad = warp & 3;         // TMEM lanes 32 * quad .. + 31
         const int half = (warp - 2) >> 2;  // half of the columns
         constexpr int kChunks = kBN / 64;  // 32-column chunks per warp
-        uint8_t* block = smem + C::kStages * C::kStageBytes + kTailBytes + (warp - 2) * kExchangeBytes;
+        uint8_t* block = smem + C::kStages * C::kStageBytes + (warp - 2) * kExchangeBytes;
         int local = 0;
         for (int t = first; t < total; t += stride, ++local) {
             const Tile ti = tile_at<kTM>(t, plan, args.n, n_tiles);
@@ -453,11 +434,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   - the leader's MMA thread issues the pair's copies and MMAs; a copy moves
 //     either CTA's own shared memory into its own tensor memory: the scales of
 //     its rows, and of all 256 columns;
-//   - the scales are turned over before, by mx_scales_kernel, into the chunks
-//     that the tensor core takes, 1 KB per 128 rows (or columns) and step, and
-//     arrive by bulk copies.  Fetched by warps of this kernel from the rows, 8 to
-//     16 bytes at a time, they bound it (8,192 rows over 8 experts, 4,096 x
-//     14,336 twice: 724 to 1,641 us by four ways of fetching them);
 //   - outputs leave by TMA through the warps' exchange blocks where all 32 rows
 //     are stored and a row of out is a multiple of 16 bytes.
 namespace mxp {
@@ -466,10 +442,6 @@ constexpr int kStages = 5;
 constexpr int kCodeBytes = 2 * 128 * 128;             // 128 rows, 128 columns
 constexpr int kStageBytes = kCodeBytes + 3 * kSfBytes;  // scales of 128 rows, 256 columns
 constexpr int kSfCols = 24, kSfBase = 256;
-constexpr int kTileRows = 256;
-constexpr int kCopyWarp = 2 + kEpiWarps;
-constexpr int kThreads = (kCopyWarp + 1) * 32;
-constexpr int kChunk = 1024;                          // a step's scales of 128 rows or columns
 
 struct __align__(16) Tail {
     uint64_t full[kStages];
@@ -505,7 +477,7 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 }  // namespace mxp
 
 template <bool kPair, bool kBf16Out>
-__global__ void __launch_bounds__(mxp::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                         const __grid_constant__ CUtensorMap tm_b2, const __grid_constant__ CUtensorMap tm_out,
                         const __grid_constant__ CUtensorMap tm_chunks, const MxGemmArgs args, const MxChunks ch,
@@ -517,7 +489,7 @@ __global__ void __launch_bounds__(mxp::kThreads, 1)
     const uint32_t rank = cluster_ctarank();
     constexpr int kColsOut = kPair ? 128 : 256;  // output columns of a tile
     const int n_tiles = (args.N + kColsOut - 1) / kColsOut;
-    const int steps = (args.K + kBK - 1) / kBK;
+    const int steps = ch.steps;
     int* status = args.status;
 
     if (threadIdx.x == 0) {
@@ -542,8 +514,8 @@ __global__ void __launch_bounds__(mxp::kThreads, 1)
         tmem_alloc_pair(smem_u32(&tail->tmem_base), kTmemCols);
         tmem_relinquish_pair();
     }
-    griddep_wait();
-    load_plan(tail->plan, args.offsets, args.n, args.R, mxp::kTileRows, status);
+    load_plan(tail->plan, args.offsets, args.n, args.R, kPairRows, status);
+    griddep_wait();  // the scales' chunks
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers exist before any remote arrive
@@ -563,9 +535,9 @@ __global__ void __launch_bounds__(mxp::kThreads, 1)
             for (int s = 0; s < mxp::kStages; ++s) armed[s] = -1;
             bool ok = true;
             for (int t = first; t < total && ok; t += stride) {
-                const Tile ti = tile_at<mxp::kTileRows>(t, plan, args.n, n_tiles);
+                const Tile ti = tile_at<kPairRows>(t, plan, args.n, n_tiles);
                 // this CTA's 128 rows, and the tile's two blocks of 128 columns
-                const int m = (ti.row0 - plan.off[ti.e]) / mxp::kTileRows;
+                const int m = (ti.row0 - plan.off[ti.e]) / kPairRows;
                 const int sa = ((plan.blk[ti.e] + m) * 2 + static_cast<int>(rank)) * steps;
                 const int cols = ch.a_blocks + ti.e * ch.col_blocks;
                 const int c0 = kPair ? ti.n_tile : 2 * ti.n_tile;
@@ -590,8 +562,8 @@ __global__ void __launch_bounds__(mxp::kThreads, 1)
                                      kPair ? ti.n_tile * 128 : ti.n_tile * 256 + r128, ti.e);
                     const uint32_t sf = base + mxp::kCodeBytes;
                     tma_load_2d_pair(sf, &tm_chunks, full, 0, sa + ks);
-                    tma_load_2d_pair(sf + mxp::kChunk, &tm_chunks, full, 0, sb0 + ks);
-                    tma_load_2d_pair(sf + 2 * mxp::kChunk, &tm_chunks, full, 0, sb1 + ks);
+                    tma_load_2d_pair(sf + kSfBytes, &tm_chunks, full, 0, sb0 + ks);
+                    tma_load_2d_pair(sf + 2 * kSfBytes, &tm_chunks, full, 0, sb1 + ks);
                     if (++stage == mxp::kStages) {
                         stage = 0;
                         phase ^= 1u;
@@ -652,7 +624,7 @@ __global__ void __launch_bounds__(mxp::kThreads, 1)
             tc_commit_pair(mapa_shared(smem_u32(&tail->done), 0));
             mbar_wait(smem_u32(&tail->done), 0, status, kStatusTimeoutDrain);
         }
-    } else if (warp == mxp::kCopyWarp) {
+    } else if (warp == kCopyWarp) {
         if (lane == 0 && rank == 0) {
             // ---------------- scales into tensor memory (leader) ----------------
             // A stage's columns are written again only after its next full barrier,
@@ -696,7 +668,7 @@ __global__ void __launch_bounds__(mxp::kThreads, 1)
         int turn = 0;
         uint32_t use = 0;
         for (int t = first; t < total; t += stride, ++use) {
-            const Tile ti = tile_at<mxp::kTileRows>(t, plan, args.n, n_tiles);
+            const Tile ti = tile_at<kPairRows>(t, plan, args.n, n_tiles);
             if (!mbar_wait(smem_u32(&tail->accum_full), use & 1u, status, kStatusTimeoutAccum)) break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
@@ -762,28 +734,28 @@ __global__ void __launch_bounds__(mxp::kThreads, 1)
     }
 }
 
-// Scales [rows][nb] -> chunks [128-row block][step][1024]: per 128 of K (half a
-// step) 512 bytes with row r's four at 16 (r % 32) + 4 (r / 32).  One block of
-// threads per 128-row block: of A (in the order of the product's row tiles), then
-// of W, then of P.
+// Scales [rows][nb] -> chunks [block][step][1024].  One block of threads per
+// chunk row: the row blocks of A in the order of the product's tiles (ch.tile_rows
+// rows each, 256 as two blocks of 128), then the 128-column blocks of W, then of P.
 __global__ void __launch_bounds__(256) mx_scales_kernel(const MxGemmArgs args, const MxChunks ch) {
     __shared__ SegmentPlan plan;
     __shared__ uint32_t slab[128][33];
-    griddep_wait();
-    load_plan(plan, args.offsets, args.n, args.R, mxp::kTileRows, args.status);
     griddep_launch_dependents();
+    griddep_wait();
     const int nb = args.K / 32, steps = ch.steps;
     int64_t block = blockIdx.x;
-    uint8_t* dst = ch.base + block * steps * mxp::kChunk;
+    uint8_t* dst = ch.base + block * steps * kSfBytes;
     const uint8_t* src;  // the block's first row, and how many it has
     int rows;
     if (block < ch.a_blocks) {
-        const int tile = static_cast<int>(block / 2);
+        load_plan(plan, args.offsets, args.n, args.R, ch.tile_rows, args.status);
+        const int halves = ch.tile_rows == kPairRows ? 2 : 1, height = ch.tile_rows / halves;
+        const int tile = static_cast<int>(block / halves);
         if (tile >= plan.blk[args.n]) return;
         const int e = plan_expert(plan, args.n, tile);
-        const int64_t row = static_cast<int64_t>(plan.off[e]) + static_cast<int64_t>(tile - plan.blk[e]) * mxp::kTileRows +
-                            128 * (block & 1);
-        rows = static_cast<int>(min(static_cast<int64_t>(128), plan.off[e + 1] - row));
+        const int64_t row = static_cast<int64_t>(plan.off[e]) +
+                            static_cast<int64_t>(tile - plan.blk[e]) * ch.tile_rows + height * (block % halves);
+        rows = static_cast<int>(min(static_cast<int64_t>(height), plan.off[e + 1] - row));
         src = args.a_scales + row * nb;
     } else {
         block -= ch.a_blocks;
@@ -821,24 +793,32 @@ __global__ void __launch_bounds__(256) mx_scales_kernel(const MxGemmArgs args, c
         // 16 bytes: rows i, i + 32, i + 64, i + 96 of one word
         for (int u = threadIdx.x; u < n_steps * 64; u += 256) {
             const int i = u & 31, q = u >> 5;
-            reinterpret_cast<uint4*>(dst + static_cast<int64_t>(s0) * mxp::kChunk)[u] =
+            reinterpret_cast<uint4*>(dst + static_cast<int64_t>(s0) * kSfBytes)[u] =
                 make_uint4(slab[i][q], slab[i + 32][q], slab[i + 64][q], slab[i + 96][q]);
         }
         __syncthreads();
     }
 }
 
-int mx_gemm_tile_rows(int64_t R, int n) { return R <= 32 * static_cast<int64_t>(n) ? 32 : 128; }
-
-bool mx_gemm_uses_pairs(const MxGemmArgs& a, int num_sms) {
-    const int64_t cols = a.b2_codes ? 128 : 256;
-    return a.R >= 256 * static_cast<int64_t>(a.n) && (a.R / 256) * ((a.N + cols - 1) / cols) >= num_sms / 2;
+int64_t mx_gemm_most_chunks(int64_t R, int n, int N, int K, int pair) {
+    // any tile height, for R rows or fewer: 64-row tiles have the most blocks
+    const int64_t rows = (R + 63) / 64 + 2 * static_cast<int64_t>(n);
+    return (rows + static_cast<int64_t>(n) * ((N + 127) / 128) * (1 + pair)) * ((K + kBK - 1) / kBK);
 }
 
-MxChunks mx_gemm_chunks(const MxGemmArgs& a) {
+MxChunks mx_gemm_chunks(const MxGemmArgs& a, int num_sms) {
     MxChunks ch{};
+    const int64_t pair_cols = a.b2_codes ? 128 : 256;
+    // CTA pairs where the experts average at least 256 rows and the tiles fill the
+    // pairs; 64-row tiles where they average at most 48 (ragged ones still end in
+    // their first tile mostly)
+    if (a.R >= 256 * static_cast<int64_t>(a.n) && (a.R / 256) * ((a.N + pair_cols - 1) / pair_cols) >= num_sms / 2)
+        ch.tile_rows = kPairRows;
+    else
+        ch.tile_rows = a.R <= 48 * static_cast<int64_t>(a.n) ? 64 : 128;
+    const int halves = ch.tile_rows == kPairRows ? 2 : 1;
     ch.steps = (a.K + kBK - 1) / kBK;
-    ch.a_blocks = static_cast<int>(2 * ((a.R + mxp::kTileRows - 1) / mxp::kTileRows + a.n));
+    ch.a_blocks = static_cast<int>(halves * ((a.R + ch.tile_rows - 1) / ch.tile_rows + a.n));
     ch.col_blocks = (a.N + 127) / 128;
     ch.blocks = ch.a_blocks + static_cast<int64_t>(a.n) * ch.col_blocks * (a.b2_codes ? 2 : 1);
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.a_scales) | reinterpret_cast<uintptr_t>(a.b_scales) |
@@ -855,7 +835,7 @@ static cudaError_t launch_pairs(const CUtensorMap* m, const MxGemmArgs& a, const
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms / 2 * 2));
-    cfg.blockDim = dim3(mxp::kThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = mxp::kSmemBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -872,19 +852,9 @@ static cudaError_t launch_pairs(const CUtensorMap* m, const MxGemmArgs& a, const
                               a.N % (kBf16Out ? 8 : 4) == 0 ? 1 : 0);
 }
 
-cudaError_t launch_mx_gemm_pairs(const CUtensorMap* m, const MxGemmArgs& a, bool bf16_out, const MxChunks& ch,
-                                 int num_sms, cudaStream_t st) {
-    cudaError_t e = launch_k(mx_scales_kernel, dim3(static_cast<unsigned>(ch.blocks)), dim3(256), 0, st, a, ch);
-    if (e != cudaSuccess) return e;
-    if (a.b2_codes)
-        return bf16_out ? launch_pairs<true, true>(m, a, ch, num_sms, st)
-                        : launch_pairs<true, false>(m, a, ch, num_sms, st);
-    return bf16_out ? launch_pairs<false, true>(m, a, ch, num_sms, st)
-                    : launch_pairs<false, false>(m, a, ch, num_sms, st);
-}
-
 template <bool kPair, bool kBf16Out, int kBN, int kTM>
-static cudaError_t launch(const CUtensorMap* m, const MxGemmArgs& a, int num_sms, cudaStream_t st) {
+static cudaError_t launch(const CUtensorMap* m, const MxGemmArgs& a, const MxChunks& ch, int num_sms,
+                          cudaStream_t st) {
     constexpr int smem = smem_bytes<kBN, kTM>();
     static_assert(smem <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<kPair, kBf16Out, kBN, kTM>,
@@ -893,32 +863,36 @@ static cudaError_t launch(const CUtensorMap* m, const MxGemmArgs& a, int num_sms
     const int64_t n_tiles = (a.N + (kPair ? 128 : kBN) - 1) / (kPair ? 128 : kBN);
     int64_t g = ((a.R + kTM - 1) / kTM + a.n) * n_tiles;
     if (g > num_sms) g = num_sms;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(a.a_scales) | reinterpret_cast<uintptr_t>(a.b_scales) |
-                         reinterpret_cast<uintptr_t>(a.b2_scales) | static_cast<uintptr_t>(a.K / 32);
-    const int how = at % 16 == 0 ? 4 : (at % 4 == 0 ? 2 : 1);
     return launch_k(mx_gemm_kernel<kPair, kBf16Out, kBN, kTM>, dim3(static_cast<unsigned>(g)), dim3(kThreads), smem,
-                    st, m[0], m[1], m[2], a, how);
+                    st, m[0], m[1], m[2], m[4], a, ch);
 }
 
-template <bool kPair, bool kBf16Out, int kBN>
-static cudaError_t launch_rows(const CUtensorMap* m, const MxGemmArgs& a, int num_sms, cudaStream_t st) {
-    return mx_gemm_tile_rows(a.R, a.n) == 32 ? launch<kPair, kBf16Out, kBN, 32>(m, a, num_sms, st)
-                                             : launch<kPair, kBf16Out, kBN, 128>(m, a, num_sms, st);
-}
-
-cudaError_t launch_mx_gemm(const CUtensorMap* m, const MxGemmArgs& a, bool bf16_out, int num_sms, cudaStream_t st) {
-    if (a.b2_codes)
-        return bf16_out ? launch_rows<true, true, 256>(m, a, num_sms, st)
-                        : launch_rows<true, false, 256>(m, a, num_sms, st);
+template <bool kBf16Out, int kTM>
+static cudaError_t launch_single(const CUtensorMap* m, const MxGemmArgs& a, const MxChunks& ch, int num_sms,
+                                 cudaStream_t st) {
+    if (a.b2_codes) return launch<true, kBf16Out, 256, kTM>(m, a, ch, num_sms, st);
     // 256-column tiles halve the reads of A; 128-column ones are taken when the
     // wide ones would leave SMs without a tile
-    const int64_t tm = mx_gemm_tile_rows(a.R, a.n);
-    const bool wide = ((a.R + tm - 1) / tm) * ((a.N + 255) / 256) >= num_sms;
-    if (wide)
-        return bf16_out ? launch_rows<false, true, 256>(m, a, num_sms, st)
-                        : launch_rows<false, false, 256>(m, a, num_sms, st);
-    return bf16_out ? launch_rows<false, true, 128>(m, a, num_sms, st)
-                    : launch_rows<false, false, 128>(m, a, num_sms, st);
+    const int64_t tiles = std::max<int64_t>((a.R + kTM - 1) / kTM, std::min<int64_t>(a.n, a.R)) * ((a.N + 255) / 256);
+    return tiles >= num_sms ? launch<false, kBf16Out, 256, kTM>(m, a, ch, num_sms, st)
+                            : launch<false, kBf16Out, 128, kTM>(m, a, ch, num_sms, st);
+}
+
+template <bool kBf16Out>
+static cudaError_t launch_product(const CUtensorMap* m, const MxGemmArgs& a, const MxChunks& ch, int num_sms,
+                                  cudaStream_t st) {
+    if (ch.tile_rows == kPairRows)
+        return a.b2_codes ? launch_pairs<true, kBf16Out>(m, a, ch, num_sms, st)
+                          : launch_pairs<false, kBf16Out>(m, a, ch, num_sms, st);
+    return ch.tile_rows == 64 ? launch_single<kBf16Out, 64>(m, a, ch, num_sms, st)
+                              : launch_single<kBf16Out, 128>(m, a, ch, num_sms, st);
+}
+
+cudaError_t launch_mx_gemm(const CUtensorMap* m, const MxGemmArgs& a, bool bf16_out, const MxChunks& ch, int num_sms,
+                           cudaStream_t st) {
+    cudaError_t e = launch_k(mx_scales_kernel, dim3(static_cast<unsigned>(ch.blocks)), dim3(256), 0, st, a, ch);
+    if (e != cudaSuccess) return e;
+    return bf16_out ? launch_product<true>(m, a, ch, num_sms, st) : launch_product<false>(m, a, ch, num_sms, st);
 }
 
 }  // namespace moe

@@ -438,25 +438,24 @@ struct MxGemmArgs {
     void* out;
     int* status;
 };
-// maps: A codes [R][K/2] in boxes of 128 bytes x mx_gemm_tile_rows rows, W and
-// the pair's codes [n][N][K/2] in boxes of 128 bytes x 128 rows.
-int mx_gemm_tile_rows(int64_t R, int n);
-// For many rows per expert (mx_gemm_uses_pairs), on CTA pairs, with the scales
-// turned over first into ch.base (ch.blocks * ch.steps KB of scratch); maps[3]:
-// out in boxes of 32 rows x 64 bytes with 64-byte swizzle, unused where a row
-// of out is no multiple of 16 bytes; maps[4]: ch.base as 32-bit words
-// [ch.blocks * ch.steps][256], a row per box.  Two launches.
+// The scales are turned over first into ch.base (ch.blocks * ch.steps KB of
+// scratch).  maps: A codes [R][K/2] in boxes of 128 bytes x min(ch.tile_rows, 128)
+// rows; W and the pair's codes [n][N][K/2] in boxes of 128 bytes x 128 rows; out
+// in boxes of 32 rows x 64 bytes with 64-byte swizzle (unused where a row of out is
+// no multiple of 16 bytes); ch.base as 32-bit words [ch.blocks * ch.steps][256], a
+// row per box.  Two launches.
 struct MxChunks {
     uint8_t* base;
-    int64_t blocks;  // of 128 rows of A, then of 128 columns of W, then of P
-    int steps;       // 1 KB each
+    int64_t blocks;  // of the rows of A, then of 128 columns of W, then of P
+    int steps;       // of 256 of K, 1 KB each
     int a_blocks, col_blocks;
+    int tile_rows;   // 64 or 128 (one CTA), 256 (CTA pairs, two blocks each)
     int words;       // the scales' rows are whole 4-byte words at 4-byte addresses
 };
-bool mx_gemm_uses_pairs(const MxGemmArgs& a, int num_sms);
-MxChunks mx_gemm_chunks(const MxGemmArgs& a);
-cudaError_t launch_mx_gemm_pairs(const CUtensorMap* maps, const MxGemmArgs& a, bool bf16_out, const MxChunks& ch,
-                                 int num_sms, cudaStream_t st);
-cudaError_t launch_mx_gemm(const CUtensorMap* maps, const MxGemmArgs& a, bool bf16_out, int num_sms, cudaStream_t st);
+MxChunks mx_gemm_chunks(const MxGemmArgs& a, int num_sms);
+// No call of up to R rows needs more KB than this.
+int64_t mx_gemm_most_chunks(int64_t R, int n, int N, int K, int pair);
+cudaError_t launch_mx_gemm(const CUtensorMap* maps, const MxGemmArgs& a, bool bf16_out, const MxChunks& ch,
+                           int num_sms, cudaStream_t st);
 
 }  // namespace moe

@@ -97,6 +97,12 @@ def test_null_handles_and_nothing_to_do(m, h):
         refused(m, call, *args, says="null handle")
     refused(m, m.moe_reserve_ffn, h, -1, 1, says="R_max = -1")
     refused(m, m.moe_reserve_ffn, h, 4, 2, says="backward = 2")
+    refused(m, m.moe_reserve_matmul_mxfp4, None, 4, 64, 64, 0, says="null handle")
+    refused(m, m.moe_reserve_matmul_mxfp4, h, -4, 64, 64, 0, says="R_max = -4")
+    refused(m, m.moe_reserve_matmul_mxfp4, h, 4, 0, 64, 0, says="N = 0")
+    refused(m, m.moe_reserve_matmul_mxfp4, h, 4, 64, 65, 0, says="K = 65")
+    refused(m, m.moe_reserve_matmul_mxfp4, h, 4, 64, 64, 3, says="pair = 3")
+    m.moe_reserve_matmul_mxfp4(h, 0, 64, 64, 1)
     # nothing to do: no pointer is looked at
     m.moe_reserve_ffn(h, 0, 1)
     m.moe_ffn_forward(h, 0, None, None, None, None, None, None, None, None, 0)

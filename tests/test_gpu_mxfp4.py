@@ -275,9 +275,15 @@ def test_under_a_captured_graph(m):
     off = torch.tensor([0, 13, 40], dtype=torch.int32).cuda()
     layer = m.MoELayer(2, 1, 64, 64, "bf16")
     try:
-        layer.reserve_ffn(1, backward=False)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
+        a = m.quantize_mxfp4(x)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            with pytest.raises(m.MoEError) as ei:  # no scratch yet, and none can be made here
+                layer.matmul_mxfp4(a, w, offsets=off)
+            assert "moe_reserve_matmul_mxfp4" in str(ei.value)
+        layer.reserve_matmul_mxfp4(40, 96, 128)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
             out = layer.matmul_mxfp4(m.quantize_mxfp4(x), w, offsets=off)
