@@ -434,16 +434,20 @@ def _refuse(where: str, message: str):
     raise MoEError(MOE_ERR_INVALID_ARG, where, message)
 
 
-def _take(where: str, name: str, t, dtype, shape):
-    """Refuse a tensor that the C ABI would misread: `t` has to be a contiguous
-    CUDA tensor of this type and shape on the current device."""
+def _device() -> int:
     import torch
-    try:  # the common case first
-        if (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda
-                and t.get_device() == torch.cuda.current_device()):
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+
+
+def _take(where: str, name: str, t, dtype, shape, dev: int):
+    """Refuse a tensor that the C ABI would misread: `t` has to be a contiguous
+    CUDA tensor of this type and shape on the current device `dev`."""
+    try:  # the common case first; get_device() is -1 for a host tensor
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
             return
     except AttributeError:
         pass
+    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _refuse(where, "%s is not a CUDA tensor" % name)
     if t.dtype != dtype:
@@ -452,7 +456,7 @@ def _take(where: str, name: str, t, dtype, shape):
         _refuse(where, "%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_contiguous():
         _refuse(where, "%s is not contiguous" % name)
-    _refuse(where, "%s is on %s, the current device is %d" % (name, t.device, torch.cuda.current_device()))
+    _refuse(where, "%s is on %s, the current device is %d" % (name, t.device, dev))
 
 
 _NO_CONTEXT = contextlib.nullcontext()
@@ -467,13 +471,13 @@ def _on(stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
-def _call_stream(s):
+def _call_stream(s, dev: int):
     """Handle of the stream to launch on, for calls whose tensors _take has
-    already found on the current CUDA device."""
+    already found on the current CUDA device `dev`."""
     if s is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the public call's time
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        return raw(dev) if raw else torch.cuda.current_stream().cuda_stream
     return _stream(s)
 
 
@@ -495,13 +499,14 @@ def quantize_mxfp4(x, values: bool = False, stream=None):
     dt = _mx_dtype(where, "x", x)
     if x.dim() < 1 or x.shape[-1] < 32 or x.shape[-1] % 32:
         _refuse(where, "x has shape %s: the last dimension must be a positive multiple of 32" % (tuple(x.shape),))
-    _take(where, "x", x, x.dtype, x.shape)
+    dev = _device()
+    _take(where, "x", x, x.dtype, x.shape, dev)
     cols, lead = x.shape[-1], x.shape[:-1]
     with _on(stream):
         codes = x.new_empty((*lead, cols // 2), dtype=torch.uint8)
         scales = x.new_empty((*lead, cols // 32), dtype=torch.uint8)
         v = torch.empty_like(x) if values else None
-    moe_quantize_mxfp4(x.numel() // cols, cols, x, dt, codes, scales, v, _call_stream(stream))
+    moe_quantize_mxfp4(x.numel() // cols, cols, x, dt, codes, scales, v, _call_stream(stream, dev))
     return (codes, scales, v) if values else (codes, scales)
 
 
@@ -515,13 +520,14 @@ def quantize_weights_mxfp4(w, values: bool = False, stream=None):
     if w.dim() != 3 or w.shape[1] < 32 or w.shape[1] % 32:
         _refuse(where, "w has shape %s: [n][rows][cols] with rows a positive multiple of 32 is wanted"
                 % (tuple(w.shape),))
-    _take(where, "w", w, w.dtype, w.shape)
+    dev = _device()
+    _take(where, "w", w, w.dtype, w.shape, dev)
     n, rows, cols = w.shape
     with _on(stream):
         codes = w.new_empty((n, cols, rows // 2), dtype=torch.uint8)
         scales = w.new_empty((n, cols, rows // 32), dtype=torch.uint8)
         v = w.new_empty((n, cols, rows)) if values else None
-    moe_quantize_weights_mxfp4(n, rows, cols, w, dt, codes, scales, v, _call_stream(stream))
+    moe_quantize_weights_mxfp4(n, rows, cols, w, dt, codes, scales, v, _call_stream(stream, dev))
     return (codes, scales, v) if values else (codes, scales)
 
 
@@ -658,17 +664,17 @@ class MoELayer:
         import torch
         return torch.bfloat16 if self.dtype == "bf16" else torch.float32
 
-    def _ffn_check(self, where, x, w1, w3, w2, offsets):
+    def _ffn_check(self, where, x, w1, w3, w2, offsets, dev):
         import torch
         dt, n, d, F = self._torch_dtype(), self.n, self.d, self.ffn
         if not isinstance(x, torch.Tensor) or x.dim() != 2:
             _refuse(where, "x is not a [rows][%d] tensor" % d)
-        _take(where, "x", x, dt, (x.shape[0], d))
-        _take(where, "w1", w1, dt, (n, d, F))
-        _take(where, "w3", w3, dt, (n, d, F))
-        _take(where, "w2", w2, dt, (n, F, d))
+        _take(where, "x", x, dt, (x.shape[0], d), dev)
+        _take(where, "w1", w1, dt, (n, d, F), dev)
+        _take(where, "w3", w3, dt, (n, d, F), dev)
+        _take(where, "w2", w2, dt, (n, F, d), dev)
         if offsets is not None:
-            _take(where, "offsets", offsets, torch.int32, (n + 1,))
+            _take(where, "offsets", offsets, torch.int32, (n + 1,), dev)
         return x.shape[0]
 
     def reserve_ffn(self, R_max: int, backward: bool = True) -> None:
@@ -684,14 +690,15 @@ class MoELayer:
         when y is allocated here)."""
         import torch
         where = "ffn_forward"
-        R = self._ffn_check(where, x, w1, w3, w2, offsets)
+        dev = _device()
+        R = self._ffn_check(where, x, w1, w3, w2, offsets, dev)
         with _on(stream):
             if y is None:
                 y = torch.empty_like(x)
             gate = x.new_empty((R, self.ffn)) if keep else None
             up = torch.empty_like(gate) if keep else None
-        _take(where, "y", y, x.dtype, x.shape)
-        moe_ffn_forward(self.h, R, offsets, x, w1, w3, w2, gate, up, y, _call_stream(stream))
+        _take(where, "y", y, x.dtype, x.shape, dev)
+        moe_ffn_forward(self.h, R, offsets, x, w1, w3, w2, gate, up, y, _call_stream(stream, dev))
         return (y, gate, up) if keep else y
 
     def ffn_backward(self, dy, x, gate, up, w1, w3, w2, offsets=None, need_dx: bool = True, need_dw: bool = True,
@@ -701,14 +708,15 @@ class MoELayer:
         need_dx=False, the weight gradients with need_dw=False."""
         import torch
         where = "ffn_backward"
-        R = self._ffn_check(where, x, w1, w3, w2, offsets)
-        _take(where, "dy", dy, x.dtype, x.shape)
-        _take(where, "gate", gate, x.dtype, (R, self.ffn))
-        _take(where, "up", up, x.dtype, (R, self.ffn))
+        dev = _device()
+        R = self._ffn_check(where, x, w1, w3, w2, offsets, dev)
+        _take(where, "dy", dy, x.dtype, x.shape, dev)
+        _take(where, "gate", gate, x.dtype, (R, self.ffn), dev)
+        _take(where, "up", up, x.dtype, (R, self.ffn), dev)
         with _on(stream):
             dx = torch.empty_like(x) if need_dx else None
             dw = [torch.empty_like(w) if need_dw else None for w in (w1, w3, w2)]
-        moe_ffn_backward(self.h, R, offsets, x, w1, w3, w2, gate, up, dy, dx, *dw, _call_stream(stream))
+        moe_ffn_backward(self.h, R, offsets, x, w1, w3, w2, gate, up, dy, dx, *dw, _call_stream(stream, dev))
         return (dx, *dw)
 
     def reserve_matmul_mxfp4(self, R_max: int, N: int, K: int, pair: bool = False) -> None:
@@ -722,7 +730,7 @@ class MoELayer:
         [n][N][K/32]) from quantize_weights_mxfp4; pair = the same of a second
         matrix: out = silu(a . w^T) * (a . pair^T).  N and K are free."""
         import torch
-        where = "matmul_mxfp4"
+        where, dev = "matmul_mxfp4", _device()
         for name, t, dims in (("a codes", a[0], 2), ("w codes", w[0], 3)):
             if not isinstance(t, torch.Tensor) or t.dim() != dims:
                 _refuse(where, "%s is not a tensor of %d dimensions" % (name, dims))
@@ -730,21 +738,21 @@ class MoELayer:
         if K < 32 or K % 32:
             _refuse(where, "K = %d is not a positive multiple of 32" % K)
         u8 = torch.uint8
-        _take(where, "a codes", a[0], u8, (R, K // 2))
-        _take(where, "a scales", a[1], u8, (R, K // 32))
+        _take(where, "a codes", a[0], u8, (R, K // 2), dev)
+        _take(where, "a scales", a[1], u8, (R, K // 32), dev)
         for name, m in (("w", w), ("pair", pair)):
             if m is not None:
-                _take(where, name + " codes", m[0], u8, (self.n, N, K // 2))
-                _take(where, name + " scales", m[1], u8, (self.n, N, K // 32))
+                _take(where, name + " codes", m[0], u8, (self.n, N, K // 2), dev)
+                _take(where, name + " scales", m[1], u8, (self.n, N, K // 32), dev)
         if offsets is not None:
-            _take(where, "offsets", offsets, torch.int32, (self.n + 1,))
+            _take(where, "offsets", offsets, torch.int32, (self.n + 1,), dev)
         dt = self._torch_dtype()
         if out is None:
             with _on(stream):
                 out = a[0].new_empty((R, N), dtype=dt)
-        _take(where, "out", out, dt, (R, N))
+        _take(where, "out", out, dt, (R, N), dev)
         p = pair if pair is not None else (None, None)
-        moe_matmul_mxfp4(self.h, R, N, K, offsets, *a[:2], *w[:2], *p[:2], out, _call_stream(stream))
+        moe_matmul_mxfp4(self.h, R, N, K, offsets, *a[:2], *w[:2], *p[:2], out, _call_stream(stream, dev))
         return out
 
     def set_capacity_factor(self, factor: float) -> None:
