@@ -179,7 +179,7 @@ moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t 
     if (v.bf16) {
         CUtensorMap m[4] = {};
         const int n = v.n, d = v.d, F = v.F;
-        const int few = moe::ffn_few_rows(op, a), box = few ? few : 128;
+        const int few = moe::ffn_few_rows(op, a, v.num_sms), box = few ? few : 128;
         bool ok = true;
         if (op == moe::kFfnUp)
             ok = map_rows(&m[0], a.x, a.R, d, box) && map_weights_across(&m[2], a.w1, n, d, F) &&

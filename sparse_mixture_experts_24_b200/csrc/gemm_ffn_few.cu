@@ -326,10 +326,35 @@ static cudaError_t launch_few_op(int op, const CUtensorMap* m, const FfnArgs& f,
     return cudaErrorInvalidValue;
 }
 
-int ffn_few_rows(int op, const FfnArgs& f) {
+// Which kernel takes a row product.  One tile of 32 or 128 rows has to hold an
+// expert's rows (ragged experts: up to about 1.4 times the average), for every
+// further tile reads the weights again.  Then this kernel is taken
+//   - where the other one's 256 x 256 tiles would leave SMs idle.  One expert of
+//     4,096 x 14,336, forward / hidden and input gradients: 16 rows 67 / 80 us
+//     against 130 / 183, 128 rows 90 / 160 against 132 / 188; 200 rows (two
+//     tiles) 151 / 260 against 133 / 189;
+//     (the hidden gradient in 128-row tiles is not: a thread's column-wise
+//     elementwise part over 128 rows costs more than the idle SMs; with the weight
+//     gradients after it, 128 rows 190 us against 122);
+//   - forward, where the reduction is long enough (48 steps) that a tile's start,
+//     which nothing overlaps here, does not count: 8 such experts, 64 rows 394
+//     against 476 us, 400 rows 478 against 523 (but backward, 128 rows, 560
+//     against 517); 128 experts of 2,048 x 768, 1,024 rows: 336 against 256;
+//   - forward, in 32-row tiles that make at most two rounds: 8 experts of 1,024 x
+//     2,816, 64 rows 41 against 47 us.
+int ffn_few_rows(int op, const FfnArgs& f, int num_sms) {
     if (op == kFfnDw) return 0;
-    if (f.R <= 32 * static_cast<int64_t>(f.n)) return 32;
-    if (f.R <= 96 * static_cast<int64_t>(f.n)) return 128;
+    const int64_t used = std::min<int64_t>(f.n, f.R);
+    const int64_t most = f.n == 1 ? f.R : (7 * f.R + 5 * f.n - 1) / (5 * f.n);
+    const int rows = most <= 32 ? 32 : (most <= 128 ? 128 : 0);
+    if (rows == 0 || (op == kFfnGrad && rows == 128)) return 0;
+    const bool forward = op == kFfnUp || op == kFfnDown;
+    const int cols = op == kFfnUp || op == kFfnGrad ? f.F : f.d;
+    const int steps = (op == kFfnUp || op == kFfnGrad ? f.d : (op == kFfnDown ? f.F : 2 * f.F)) / kBK;
+    const int pair_cols = op == kFfnUp ? 128 : 256;
+    if (used * ((cols + pair_cols - 1) / pair_cols) < num_sms / 2) return rows;
+    if (forward && steps >= 48) return rows;
+    if (forward && rows == 32 && used * ((cols + kBM - 1) / kBM) <= 2 * static_cast<int64_t>(num_sms)) return rows;
     return 0;
 }
 

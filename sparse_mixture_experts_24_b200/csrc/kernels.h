@@ -408,7 +408,7 @@ cudaError_t launch_ffn_maps(const CUtensorMap* maps5, const int32_t* offsets, in
 // The row ops for few rows per expert (gemm_ffn_few.cu): ffn_few_rows gives the
 // batch rows of its tiles (the box of the row operands' maps), or 0 where
 // launch_ffn_tc is to be taken.  The weights' maps are the same.
-int ffn_few_rows(int op, const FfnArgs& f);
+int ffn_few_rows(int op, const FfnArgs& f, int num_sms);
 cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, int num_sms, cudaStream_t st);
 // Output maps in 32 x 32 boxes with 64-byte swizzle: kFfnUp h, gate, up; kFfnDown
 // y; kFfnGrad da, db, h; kFfnDx dx; kFfnDw dw1, dw3, dw2 (3-D: column, row, expert).
