@@ -530,10 +530,11 @@ MOE_API moe_status moe_ep_buffer_close(void *ptr, int opened);
  * weight gradients.  A NaN or infinity in one expert's rows stays with that
  * expert.  Outputs must not overlap inputs or one another.
  * The calls use a workspace of their own in the handle: R * ffn elements
- * forward, three times that backward.  It grows on demand (not while `stream`
- * is captured: MOE_ERR_INVALID_ARG then, so call moe_reserve_ffn first) and a
- * buffer that was replaced lives until moe_destroy, so captured graphs stay
- * valid.  Calls on one handle share it: order them, graph replays included.
+ * forward, three times that backward.  It grows on demand (the call then waits
+ * for the device; not while `stream` is captured: MOE_ERR_INVALID_ARG, so call
+ * moe_reserve_ffn first).  A buffer that a captured call used lives until
+ * moe_destroy, so its graph stays valid.  Calls on one handle share the
+ * workspace: order them, graph replays included.
  *
  * moe_reserve_ffn: room for R_max rows, for the forward pass (backward = 0) or
  * both (backward = 1).

@@ -45,67 +45,64 @@ moe_status check_offsets(int n, const int32_t* offsets) {
     return MOE_OK;
 }
 
-moe_status allocate(moe::FfnWorkspace* w, size_t bytes, cudaStream_t st, bool use_stream, void** out) {
-    if (use_stream) {
-        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-        cudaError_t e = cudaStreamIsCapturing(st, &cap);
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            return cuda_failed(e, "cudaStreamIsCapturing");
-        }
-        if (cap != cudaStreamCaptureStatusNone)
+// Whether `st` is being captured (a reservation is not on a stream).
+moe_status capturing(cudaStream_t st, bool on_stream, bool* yes) {
+    *yes = false;
+    if (!on_stream) return MOE_OK;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(st, &cap);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return cuda_failed(e, "cudaStreamIsCapturing");
+    }
+    *yes = cap != cudaStreamCaptureStatusNone;
+    return MOE_OK;
+}
+
+// At least `bytes` in b.
+moe_status room(moe::FfnWorkspace* w, moe::FfnBuffer* b, int64_t bytes, bool capture) {
+    if (bytes > b->bytes) {
+        if (capture)
             return failed(MOE_ERR_INVALID_ARG,
                           "the workspace is too small and cannot grow while the stream is captured: call "
                           "moe_reserve_ffn or moe_reserve_matmul_mxfp4 first");
+        if (b->p) {
+            if (b->captured)
+                w->kept.push_back(b->p);
+            else
+                cudaFree(b->p);
+            *b = moe::FfnBuffer{};
+        }
+        cudaError_t e = cudaMalloc(&b->p, static_cast<size_t>(bytes));
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            *b = moe::FfnBuffer{};
+            return failed(MOE_ERR_ALLOC, "cudaMalloc(%lld bytes) for the workspace failed: %s",
+                          static_cast<long long>(bytes), cudaGetErrorString(e));
+        }
+        b->bytes = bytes;
     }
-    void* p = nullptr;
-    cudaError_t e = cudaMalloc(&p, bytes);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return failed(MOE_ERR_ALLOC, "cudaMalloc(%zu bytes) for the workspace failed: %s", bytes,
-                      cudaGetErrorString(e));
-    }
-    w->allocations.push_back(p);
-    *out = p;
+    b->captured |= capture;
     return MOE_OK;
 }
 
-// The status word, allocated once; then room for `rows` hidden rows and, for
-// the backward pass, their gradients.
-moe_status need(const HandleView& v, int64_t rows, bool backward, cudaStream_t st, bool use_stream) {
+// The status word and the tensor maps; then room for `rows` hidden rows and, for
+// the backward pass, their gradients; and for `chunks` KB of turned-over scales.
+moe_status need(const HandleView& v, int64_t rows, bool backward, int64_t chunks, cudaStream_t st, bool on_stream) {
     moe::FfnWorkspace* w = v.ffn;
-    if (!w->status) {
-        void* p = nullptr;
-        moe_status s = allocate(w, 256 + sizeof(CUtensorMap) * moe::kFfnDwMaps * v.n, st, use_stream, &p);
+    bool capture = false;
+    moe_status s = capturing(st, on_stream, &capture);
+    if (s != MOE_OK) return s;
+    if (!w->fixed.p) {
+        s = room(w, &w->fixed, 256 + static_cast<int64_t>(sizeof(CUtensorMap)) * moe::kFfnDwMaps * v.n, capture);
         if (s != MOE_OK) return s;
-        cudaError_t e = cudaMemset(p, 0, 256);
+        cudaError_t e = cudaMemset(w->fixed.p, 0, 256);
         if (e != cudaSuccess) return cuda_failed(e, "cudaMemset(status)");
-        w->status = static_cast<int*>(p);
-        w->maps = static_cast<uint8_t*>(p) + 256;
     }
-    const size_t row = static_cast<size_t>(v.F) * (v.bf16 ? 2 : 4);
-    if (rows > w->h_rows) {
-        moe_status s = allocate(w, row * rows, st, use_stream, &w->h);
-        if (s != MOE_OK) return s;
-        w->h_rows = rows;
-    }
-    if (backward && rows > w->grad_rows) {
-        void* p = nullptr;
-        moe_status s = allocate(w, 2 * row * rows, st, use_stream, &p);
-        if (s != MOE_OK) return s;
-        w->da = p;
-        w->db = static_cast<uint8_t*>(p) + row * rows;
-        w->grad_rows = rows;
-    }
-    return MOE_OK;
-}
-
-// Scratch for `chunks` KB of scales of the MXFP4 product.
-moe_status need_chunks(const HandleView& v, int64_t chunks, cudaStream_t st, bool use_stream) {
-    moe::FfnWorkspace* w = v.ffn;
-    if (chunks * 1024 <= w->chunk_bytes) return MOE_OK;
-    moe_status s = allocate(w, static_cast<size_t>(chunks) * 1024, st, use_stream, &w->chunks);
-    if (s == MOE_OK) w->chunk_bytes = chunks * 1024;
+    const int64_t row = static_cast<int64_t>(v.F) * (v.bf16 ? 2 : 4);
+    if (rows > 0) s = room(w, &w->hidden, row * rows, capture);
+    if (s == MOE_OK && rows > 0 && backward) s = room(w, &w->grads, 2 * row * rows, capture);
+    if (s == MOE_OK && chunks > 0) s = room(w, &w->chunks, chunks * 1024, capture);
     return s;
 }
 
@@ -116,10 +113,10 @@ moe::FfnArgs ffn_args(const HandleView& v, int64_t R, const int32_t* offsets) {
     a.R = R;
     a.d = v.d;
     a.F = v.F;
-    a.h = v.ffn->h;
-    a.da = v.ffn->da;
-    a.db = v.ffn->db;
-    a.status = v.ffn->status;
+    a.h = v.ffn->hidden.p;
+    a.da = v.ffn->grads.p;
+    a.db = static_cast<uint8_t*>(v.ffn->grads.p) + v.ffn->grads.bytes / 2;
+    a.status = v.ffn->status();
     return a;
 }
 
@@ -207,7 +204,7 @@ moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t 
             ok = map_out(&out.m[0], op == moe::kFfnDown ? a.y : a.dx, a.R, d);
         if (!ok) return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%s)", what);
         e = few ? moe::launch_ffn_few(op, few, m, a, v.num_sms, st)
-                : moe::launch_ffn_tc(op, m, out, a, v.ffn->maps, v.num_sms, st);
+                : moe::launch_ffn_tc(op, m, out, a, v.ffn->maps(), v.num_sms, st);
     } else {
         e = moe::launch_ffn_simt(op, a, v.num_sms, st);
     }
@@ -223,7 +220,7 @@ moe_status run_maps(const HandleView& v, const moe::FfnArgs& a, cudaStream_t st)
         !map_rows_across(&m[2], a.da, a.R, v.F) || !map_rows_across(&m[3], a.db, a.R, v.F) ||
         !map_rows_across(&m[4], a.dy, a.R, v.d))
         return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (weight gradients)");
-    cudaError_t e = moe::launch_ffn_maps(m, a.offsets, v.n, a.R, v.ffn->maps, a.status, st);
+    cudaError_t e = moe::launch_ffn_maps(m, a.offsets, v.n, a.R, v.ffn->maps(), a.status, st);
     if (e != cudaSuccess) return cuda_failed(e, "tensor map launch");
     *v.launches += 1;
     return MOE_OK;
@@ -243,7 +240,7 @@ moe_status moe_reserve_ffn(moe_handle* h, int64_t R_max, int backward) {
     HandleView v;
     s = open_handle(h, &v);
     if (s != MOE_OK) return s;
-    s = need(v, R_max, backward == 1, nullptr, false);
+    s = need(v, R_max, backward == 1, 0, nullptr, false);
     return s == MOE_OK ? done() : s;
 }
 
@@ -270,7 +267,7 @@ moe_status moe_ffn_forward(moe_handle* h, int64_t R, const int32_t* offsets, con
     s = check_offsets(v.n, offsets);
     if (s != MOE_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    s = need(v, R, false, st, true);
+    s = need(v, R, false, 0, st, true);
     if (s != MOE_OK) return s;
     moe::FfnArgs a = ffn_args(v, R, offsets);
     a.x = x;
@@ -325,7 +322,7 @@ moe_status moe_ffn_backward(moe_handle* h, int64_t R, const int32_t* offsets, co
     }
     s = check_offsets(v.n, offsets);
     if (s != MOE_OK) return s;
-    s = need(v, R, true, st, true);
+    s = need(v, R, true, 0, st, true);
     if (s != MOE_OK) return s;
     moe::FfnArgs a = ffn_args(v, R, offsets);
     a.x = x;
@@ -430,9 +427,7 @@ moe_status moe_reserve_matmul_mxfp4(moe_handle* h, int64_t R_max, int N, int K, 
     HandleView v;
     s = open_handle(h, &v);
     if (s != MOE_OK) return s;
-    s = need(v, 0, false, nullptr, false);
-    if (s != MOE_OK) return s;
-    s = need_chunks(v, moe::mx_gemm_most_chunks(R_max, v.n, N, K, pair), nullptr, false);
+    s = need(v, 0, false, moe::mx_gemm_most_chunks(R_max, v.n, N, K, pair), nullptr, false);
     return s == MOE_OK ? done() : s;
 }
 
@@ -459,14 +454,13 @@ moe_status moe_matmul_mxfp4(moe_handle* h, int64_t R, int N, int K, const int32_
     s = check_offsets(v.n, offsets);
     if (s != MOE_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    s = need(v, 0, false, st, true);
-    if (s != MOE_OK) return s;
-    moe::MxGemmArgs a{offsets,  v.n,      R,          N,           K,   a_codes,      a_scales,
-                      w_codes,  w_scales, pair_codes, pair_scales, out, v.ffn->status};
+    moe::MxGemmArgs a{offsets,  v.n,      R,          N,           K,   a_codes, a_scales,
+                      w_codes,  w_scales, pair_codes, pair_scales, out, nullptr};
     moe::MxChunks ch = moe::mx_gemm_chunks(a, v.num_sms);
-    s = need_chunks(v, ch.blocks * ch.steps, st, true);
+    s = need(v, 0, false, ch.blocks * ch.steps, st, true);
     if (s != MOE_OK) return s;
-    ch.base = static_cast<uint8_t*>(v.ffn->chunks);
+    a.status = v.ffn->status();
+    ch.base = static_cast<uint8_t*>(v.ffn->chunks.p);
     const uint64_t k2 = static_cast<uint64_t>(K) / 2, cols = static_cast<uint64_t>(N);
     const uint64_t a_dims[2] = {k2, static_cast<uint64_t>(R)}, a_strides[1] = {k2};
     const uint32_t a_box[2] = {128, ch.tile_rows < 128 ? static_cast<uint32_t>(ch.tile_rows) : 128u};

@@ -13,20 +13,24 @@
 
 namespace moe {
 
-// Workspace of the feed-forward block.  Buffers grow, but a buffer that a
-// larger one replaces stays allocated until moe_destroy: kernels in flight and
-// captured graphs may still use it.  The status word never moves.
+// A buffer of the workspace.  It grows on demand: what a larger one replaces is
+// freed (which waits for the device), unless a captured call used it -- a graph
+// may replay with it, so it stays until moe_destroy.
+struct FfnBuffer {
+    void* p = nullptr;
+    int64_t bytes = 0;
+    bool captured = false;
+};
+
+// Workspace of the feed-forward block and the MXFP4 product.
 struct FfnWorkspace {
-    int* status = nullptr;
-    void* maps = nullptr;      // device tensor maps of the weight gradients
-    void* h = nullptr;         // [rows][F]
-    int64_t h_rows = 0;
-    void* da = nullptr;        // [grad_rows][F]
-    void* db = nullptr;
-    int64_t grad_rows = 0;
-    void* chunks = nullptr;    // scales of the MXFP4 product, turned over
-    int64_t chunk_bytes = 0;
-    std::vector<void*> allocations;
+    FfnBuffer fixed;   // status word, then the tensor maps of the weight gradients; never grows
+    FfnBuffer hidden;  // h [rows][F]
+    FfnBuffer grads;   // da, db [rows][F]
+    FfnBuffer chunks;  // scales of the MXFP4 product, turned over
+    std::vector<void*> kept;  // replaced, but used by captured calls
+    int* status() const { return static_cast<int*>(fixed.p); }
+    void* maps() const { return fixed.p ? static_cast<uint8_t*>(fixed.p) + 256 : nullptr; }
 };
 
 }  // namespace moe

@@ -1805,7 +1805,7 @@ moe_status moe_sync_status(moe_handle* h, moe_stream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "pending CUDA error");
     int st = 0;
-    for (int* word : {h->status, h->ffn.status}) {
+    for (int* word : {h->status, h->ffn.status()}) {
         if (!word) continue;
         int v = 0;
         e = cudaMemcpy(&v, word, sizeof v, cudaMemcpyDeviceToHost);
@@ -1896,7 +1896,9 @@ moe_status moe_destroy(moe_handle* h) {
     if (!h) return ok();
     trace_free(h);
     if (h->ws) cudaFree(h->ws);
-    for (void* p : h->ffn.allocations) cudaFree(p);
+    for (void* p : {h->ffn.fixed.p, h->ffn.hidden.p, h->ffn.grads.p, h->ffn.chunks.p})
+        if (p) cudaFree(p);
+    for (void* p : h->ffn.kept) cudaFree(p);
     delete h;
     return ok();
 }
