@@ -483,6 +483,9 @@ def _call_stream(s, dev: int):
 
 def _mx_dtype(where: str, name: str, t):
     import torch
+    dtype = getattr(t, "dtype", None)  # the common case first; _take sees to the rest
+    if dtype is torch.bfloat16 and t.is_cuda:
+        return MOE_BF16
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _refuse(where, "%s is not a CUDA tensor" % name)
     if t.dtype not in (torch.bfloat16, torch.float32):
@@ -495,18 +498,22 @@ def quantize_mxfp4(x, values: bool = False, stream=None):
     cols -> (codes uint8 [..., cols/2], scales uint8 [..., cols/32]), and with
     values=True also the tensor that they stand for, in x's type."""
     import torch
-    where = "quantize_mxfp4"
+    where, dev = "quantize_mxfp4", _device()
     dt = _mx_dtype(where, "x", x)
-    if x.dim() < 1 or x.shape[-1] < 32 or x.shape[-1] % 32:
-        _refuse(where, "x has shape %s: the last dimension must be a positive multiple of 32" % (tuple(x.shape),))
-    dev = _device()
-    _take(where, "x", x, x.dtype, x.shape, dev)
-    cols, lead = x.shape[-1], x.shape[:-1]
+    shape = x.shape
+    cols = shape[-1] if len(shape) else 0
+    if cols < 32 or cols % 32:
+        _refuse(where, "x has shape %s: the last dimension must be a positive multiple of 32" % (tuple(shape),))
+    _take(where, "x", x, x.dtype, shape, dev)
+    lead = shape[:-1]
     with _on(stream):
         codes = x.new_empty((*lead, cols // 2), dtype=torch.uint8)
         scales = x.new_empty((*lead, cols // 32), dtype=torch.uint8)
         v = torch.empty_like(x) if values else None
-    moe_quantize_mxfp4(x.numel() // cols, cols, x, dt, codes, scales, v, _call_stream(stream, dev))
+    rc = lib.moe_quantize_mxfp4(x.numel() // cols, cols, x.data_ptr(), dt, codes.data_ptr(), scales.data_ptr(),
+                                v.data_ptr() if values else None, _call_stream(stream, dev))
+    if rc:
+        _check(rc, "moe_quantize_mxfp4")
     return (codes, scales, v) if values else (codes, scales)
 
 
@@ -752,7 +759,8 @@ class MoELayer:
                 out = a[0].new_empty((R, N), dtype=dt)
         _take(where, "out", out, dt, (R, N), dev)
         p = pair if pair is not None else (None, None)
-        moe_matmul_mxfp4(self.h, R, N, K, offsets, *a[:2], *w[:2], *p[:2], out, _call_stream(stream, dev))
+        moe_matmul_mxfp4(self.h, R, N, K, offsets, a[0], a[1], w[0], w[1], p[0], p[1], out,
+                         _call_stream(stream, dev))
         return out
 
     def set_capacity_factor(self, factor: float) -> None:

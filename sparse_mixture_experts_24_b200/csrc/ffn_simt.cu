@@ -13,8 +13,8 @@
 // step a thread reads 16 values from shared memory for 64 multiply-adds.  The
 // 128 columns are two halves of 64 (thread columns 4 tx .. 4 tx + 3 of either),
 // so that the pairs a, b and da, db of one hidden column meet in one thread.
-// The reduction runs in chunks of 16 through two shared-memory buffers, the
-// next chunk's global loads in flight while the current one is multiplied.
+// The reduction runs in chunks of 16 through three shared-memory buffers, the
+// next two chunks' asynchronous copies in flight while one is multiplied.
 // One warp per scheduler issues a multiply-add every other cycle at best, and
 // small batches have fewer tiles than SMs: a row product is then split along
 // its reduction over a cluster of up to 8 blocks, whose partial sums meet in
@@ -30,6 +30,20 @@ namespace moe {
 namespace ffn_simt {
 
 constexpr int kM = 64, kN = 128, kK = 16, kThreads = 128;
+constexpr int kBuffers = 3;
+
+__device__ __forceinline__ const float* at(const void* p, int64_t i) { return static_cast<const float*>(p) + i; }
+
+// Asynchronous copies into shared memory; zeros instead where `in` is false (the
+// source is not read then).
+__device__ __forceinline__ void copy4(float* dst, const float* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
 
 __device__ __forceinline__ float4 load4(const void* p, int64_t i) {
     return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
@@ -50,8 +64,8 @@ __device__ __forceinline__ void store4(void* p, int64_t i, float a, float b, flo
 }
 
 struct Tiles {
-    float a[2][kK][kM + 4];  // rows of both arrays stay 16-byte aligned: they are read as float4
-    float b[2][kK][kN + 4];
+    float a[kBuffers][kK][kM + 4];  // rows of both arrays stay 16-byte aligned: they are read as float4
+    float b[kBuffers][kK][kN + 4];
 };
 struct __align__(16) Smem {
     union {
@@ -108,88 +122,56 @@ __global__ void __launch_bounds__(kThreads, kOp == kFfnGrad || kOp == kFfnDx ? 4
     const int64_t w_at = static_cast<int64_t>(e) * d * F;
     const int64_t seg0 = kOp == kFfnDw ? sm.plan.off[e] : 0;
 
-    // this thread's four-element pieces of a chunk: 2 of A (64 x 16), 4 of B (16 x 128)
-    float4 ra[2], rb[4];
-    auto fetch = [&](int64_t k0) {
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    // Copies of chunk c (16 of the reduction) into buffer `buf`: 16 bytes where the
+    // operand lies along the tile's rows or columns, element by element where it
+    // lies along the reduction and has to be turned over; zeros past the segment.
+    auto issue = [&](int64_t c, int buf) {
+        int64_t k0 = c * kK;
+        const bool second = kOp == kFfnDx && k0 >= F;  // F is a multiple of 16
+        if (second) k0 -= F;
+        if (kOp == kFfnDw) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int p = tid + i * kThreads;
-            if (kOp == kFfnDw) {  // A(m, k) = row k of x (or h), feature m: 16 pieces of a row
-                const int64_t k = k0 + (p >> 4);
-                const int m = row0 + (p & 15) * 4;
-                ra[i] = k < K ? (dw2 ? load4(g.h, (seg0 + k) * F + m) : load4(g.x, (seg0 + k) * d + m)) : zero;
-            } else {
-                const int r = p >> 2;
-                const int64_t k = k0 + (p & 3) * 4;
-                const int64_t row = static_cast<int64_t>(row0) + r;
-                if (r >= rows)
-                    ra[i] = zero;
-                else if (kOp == kFfnUp)
-                    ra[i] = load4(g.x, row * d + k);
-                else if (kOp == kFfnDown)
-                    ra[i] = load4(g.h, row * F + k);
-                else if (kOp == kFfnGrad)
-                    ra[i] = load4(g.dy, row * d + k);
-                else
-                    ra[i] = k < F ? load4(g.da, row * F + k) : load4(g.db, row * F + k - F);
+            for (int i = 0; i < 2; ++i) {
+                const int p = tid + i * kThreads, k = p >> 4, m = (p & 15) * 4;
+                const bool in = k0 + k < K;
+                const int64_t row = seg0 + (in ? k0 + k : 0);
+                copy16(&sm.t.a[buf][k][m], dw2 ? at(g.h, row * F + row0 + m) : at(g.x, row * d + row0 + m), in);
+            }
+        } else {
+            const int k = tid & 15, ld = kOp == kFfnUp || kOp == kFfnGrad ? d : F;
+            const void* base = kOp == kFfnUp     ? g.x
+                               : kOp == kFfnDown ? g.h
+                               : kOp == kFfnGrad ? g.dy
+                                                 : (second ? g.db : g.da);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = (tid >> 4) + 8 * i;
+                const bool in = r < rows;
+                copy4(&sm.t.a[buf][k][r], at(base, (static_cast<int64_t>(row0) + (in ? r : 0)) * ld + k0 + k), in);
             }
         }
+        if (kOp == kFfnGrad || kOp == kFfnDx) {  // B(n, k): the weights' rows, k contiguous
+            const int k = tid & 15, ld = kOp == kFfnGrad ? d : F;
+            const void* base = kOp == kFfnGrad ? g.w2 : (second ? g.w3 : g.w1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int p = tid + i * kThreads;
-            if (kOp == kFfnGrad || kOp == kFfnDx) {  // B(n, k): the weights' rows, k contiguous
-                const int n = p >> 2;
-                const int64_t k = k0 + (p & 3) * 4;
-                const int64_t c = col[n >> 6] + (n & 63);
-                if (c >= cols)
-                    rb[i] = zero;
-                else if (kOp == kFfnGrad)
-                    rb[i] = load4(g.w2, w_at + c * d + k);
-                else
-                    rb[i] = k < F ? load4(g.w1, w_at + c * F + k) : load4(g.w3, w_at + c * F + k - F);
-            } else {  // n contiguous
+            for (int i = 0; i < 16; ++i) {
+                const int n = (tid >> 4) + 8 * i, c0 = col[0] + n;  // the halves adjoin
+                const bool in = c0 < cols;
+                copy4(&sm.t.b[buf][k][n], at(base, w_at + static_cast<int64_t>(in ? c0 : 0) * ld + k0 + k), in);
+            }
+        } else {  // n contiguous
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int p = tid + i * kThreads, n = (p & 31) * 4, half = n >> 6;
                 const int64_t k = k0 + (p >> 5);
-                const int n = (p & 31) * 4, half = n >> 6;
-                const int64_t c = col[half] + (n & 63);
-                if (c >= cols || k >= K)
-                    rb[i] = zero;
-                else if (kOp == kFfnUp)
-                    rb[i] = load4(half ? g.w3 : g.w1, w_at + k * F + c);
-                else if (kOp == kFfnDown)
-                    rb[i] = load4(g.w2, w_at + k * d + c);
-                else if (dw2)
-                    rb[i] = load4(g.dy, (seg0 + k) * d + c);
-                else
-                    rb[i] = load4(half ? g.db : g.da, (seg0 + k) * F + c);
-            }
-        }
-    };
-    auto put = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int p = tid + i * kThreads;
-            if (kOp == kFfnDw) {
-                *reinterpret_cast<float4*>(&sm.t.a[buf][p >> 4][(p & 15) * 4]) = ra[i];
-            } else {
-                const int r = p >> 2, k = (p & 3) * 4;
-                sm.t.a[buf][k][r] = ra[i].x;
-                sm.t.a[buf][k + 1][r] = ra[i].y;
-                sm.t.a[buf][k + 2][r] = ra[i].z;
-                sm.t.a[buf][k + 3][r] = ra[i].w;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int p = tid + i * kThreads;
-            if (kOp == kFfnGrad || kOp == kFfnDx) {
-                const int n = p >> 2, k = (p & 3) * 4;
-                sm.t.b[buf][k][n] = rb[i].x;
-                sm.t.b[buf][k + 1][n] = rb[i].y;
-                sm.t.b[buf][k + 2][n] = rb[i].z;
-                sm.t.b[buf][k + 3][n] = rb[i].w;
-            } else {
-                *reinterpret_cast<float4*>(&sm.t.b[buf][p >> 5][(p & 31) * 4]) = rb[i];
+                const int c0 = col[half] + (n & 63);
+                const bool in = c0 < cols && k < K;
+                const int64_t kk = in ? k : 0, cc = in ? c0 : 0;
+                const float* src = kOp == kFfnUp     ? at(half ? g.w3 : g.w1, w_at + kk * F + cc)
+                                   : kOp == kFfnDown ? at(g.w2, w_at + kk * d + cc)
+                                   : dw2             ? at(g.dy, (seg0 + kk) * d + cc)
+                                                     : at(half ? g.db : g.da, (seg0 + kk) * F + cc);
+                copy16(&sm.t.b[buf][p >> 5][n], src, in);
             }
         }
     };
@@ -203,14 +185,18 @@ __global__ void __launch_bounds__(kThreads, kOp == kFfnGrad || kOp == kFfnDx ? 4
     const int rank = kOp == kFfnDw ? 0 : static_cast<int>(blockIdx.x) % splits;
     const int64_t all = (K + kK - 1) / kK, c0 = kOp == kFfnDw ? 0 : all * rank / splits;
     const int64_t chunks = kOp == kFfnDw ? all : all * (rank + 1) / splits - c0;
-    if (chunks > 0) {
-        fetch(c0 * kK);
-        put(0);
+    // kBuffers - 1 chunks ahead; an empty group keeps the count where there is none
+#pragma unroll
+    for (int i = 0; i < kBuffers - 1; ++i) {
+        if (i < chunks) issue(c0 + i, i);
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    __syncthreads();
+    int buf = 0;
     for (int64_t c = 0; c < chunks; ++c) {
-        const int buf = static_cast<int>(c & 1);
-        if (c + 1 < chunks) fetch((c0 + c + 1) * kK);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kBuffers - 2) : "memory");
+        __syncthreads();  // chunk c is there for all, and all have done with chunk c - 1
+        if (c + kBuffers - 1 < chunks) issue(c0 + c + kBuffers - 1, buf == 0 ? kBuffers - 1 : buf - 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
             const float4 a0 = *reinterpret_cast<const float4*>(&sm.t.a[buf][k][ty * 8]);
@@ -226,9 +212,9 @@ __global__ void __launch_bounds__(kThreads, kOp == kFfnGrad || kOp == kFfnDx ? 4
                 for (int j = 0; j < 4; ++j) fma2(acc2[i][j], a2, bv[j]);
             }
         }
-        if (c + 1 < chunks) put(buf ^ 1);
-        __syncthreads();
+        if (++buf == kBuffers) buf = 0;
     }
+    __syncthreads();  // the buffers hold the partial sums next
 
     float acc[8][8];
 #pragma unroll
@@ -316,9 +302,9 @@ template <int kOp>
 static cudaError_t launch_row_op(const FfnArgs& a, int column_tiles, int K, int num_sms, cudaStream_t st) {
     const int64_t blocks = (a.R + kM - 1) / kM + a.n;  // at most
     const int64_t likely = std::max<int64_t>((a.R + kM - 1) / kM, std::min<int64_t>(a.n, a.R));
-    // up to 4 blocks per SM run together
+    // 3 or 4 blocks per SM run together; twice as many even out over the SMs
     int splits = 1;
-    while (splits < 8 && likely * column_tiles * splits * 2 <= 4 * num_sms && K / kK >= 8 * splits) splits *= 2;
+    while (splits < 8 && likely * column_tiles * splits * 2 <= 8 * num_sms && K / kK >= 8 * splits) splits *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks * splits), static_cast<unsigned>(column_tiles));
     cfg.blockDim = dim3(kThreads);

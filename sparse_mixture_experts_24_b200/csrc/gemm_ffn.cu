@@ -541,7 +541,8 @@ cudaError_t launch_ffn_maps(const CUtensorMap* maps5, const int32_t* offsets, in
 template <int kOp>
 static cudaError_t launch_op(const CUtensorMap* m, const FfnOutMaps& out, const FfnTcArgs& a, int64_t max_tiles, int num_sms,
                              cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(ffn_tc_kernel<kOp>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(ffn_tc_kernel<kOp>), kSmemBytes, done);
     if (e != cudaSuccess) return e;
     int64_t pairs = num_sms / 2;
     if (max_tiles < pairs) pairs = max_tiles;

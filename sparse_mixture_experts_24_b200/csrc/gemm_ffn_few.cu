@@ -287,7 +287,8 @@ template <int kOp, int kT>
 static cudaError_t launch_few(const CUtensorMap* m, const FfnArgs& f, int num_sms, cudaStream_t st) {
     constexpr int smem = smem_bytes<kOp, kT>();
     static_assert(smem <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(ffn_few_kernel<kOp, kT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(ffn_few_kernel<kOp, kT>), smem, done);
     if (e != cudaSuccess) return e;
     const int cols = kOp == kFfnUp || kOp == kFfnGrad ? f.F : f.d;
     const int K = kOp == kFfnUp || kOp == kFfnGrad ? f.d : (kOp == kFfnDown ? f.F : 2 * f.F);

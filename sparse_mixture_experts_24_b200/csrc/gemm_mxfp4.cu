@@ -833,8 +833,8 @@ MxChunks mx_gemm_chunks(const MxGemmArgs& a, int num_sms) {
 template <bool kPair, bool kBf16Out>
 static cudaError_t launch_pairs(const CUtensorMap* m, const MxGemmArgs& a, const MxChunks& ch, int num_sms,
                                 cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(mx_gemm_pair_kernel<kPair, kBf16Out>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, mxp::kSmemBytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(mx_gemm_pair_kernel<kPair, kBf16Out>), mxp::kSmemBytes, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms / 2 * 2));
@@ -860,8 +860,8 @@ static cudaError_t launch(const CUtensorMap* m, const MxGemmArgs& a, const MxChu
                           cudaStream_t st) {
     constexpr int smem = smem_bytes<kBN, kTM>();
     static_assert(smem <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<kPair, kBf16Out, kBN, kTM>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(mx_gemm_kernel<kPair, kBf16Out, kBN, kTM>), smem, done);
     if (e != cudaSuccess) return e;
     const int64_t n_tiles = (a.N + (kPair ? 128 : kBN) - 1) / (kPair ? 128 : kBN);
     int64_t g = ((a.R + kTM - 1) / kTM + a.n) * n_tiles;

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace moe {
 
 // Kernels launched by one API call form a chain on its stream; every launch
@@ -30,6 +32,19 @@ inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
     cfg.numAttrs = (g_chain_started && pdl_enabled()) ? 1 : 0;
     g_chain_started = true;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Allow `kernel` its dynamic shared memory, once per device (`done`: a bit per
+// device, static at the launch).
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // Rows of one M-block of the tensor-core GEMMs and of the CUDA-core GEMMs.
