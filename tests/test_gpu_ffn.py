@@ -44,6 +44,7 @@ SHAPES = [
     (8, [16, 15, 17, 0, 33, 32, 31, 2], 146, 1, 1, 192, 576),
     (2, [300, 513], 813, 0, 0, 512, 256),
     (33, [7, 0, 1] * 11, 88, 0, 0, 64, 128),
+    (256, [1, 0, 2, 0] * 64, 192, 2, 1, 64, 64),
     # few rows: reductions split over clusters of 2, 4 and 8, one and several row blocks
     (1, None, 5, 0, 0, 1024, 1536),
     (1, None, 2, 0, 0, 64, 4096),
@@ -271,5 +272,70 @@ def test_refuses_tensors_that_it_would_misread(m):
         with pytest.raises(m.MoEError) as ei:
             layer.ffn_backward(t["dy"], t["x"], t["gate"][:, :64], t["up"], t["w1"], t["w3"], t["w2"], offsets=off)
         assert "gate has shape" in str(ei.value)
+    finally:
+        layer.close()
+
+
+def test_two_layers_at_once_on_two_streams(m):
+    """Handles share nothing: calls of two of them, interleaved on two streams with
+    growing batches, give what they give one after the other."""
+    n, d, F = 3, 192, 320
+    layers = [m.MoELayer(n, 1, d, F, "bf16") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    try:
+        jobs = []
+        for i, R in enumerate((40, 300, 150, 700)):
+            for k in range(2):
+                t = make(n, R, d, F, "bf16", seed=10 * i + k)
+                off = torch.tensor([0, R // 3, R // 2 + k, R], dtype=torch.int32).cuda()
+                jobs.append((k, t, off))
+        torch.cuda.synchronize()
+
+        def run(k, t, off, stream):
+            y, gate, up = layers[k].ffn_forward(t["x"], t["w1"], t["w3"], t["w2"], offsets=off, keep=True,
+                                                stream=stream)
+            return (y, *layers[k].ffn_backward(t["dy"], t["x"], gate, up, t["w1"], t["w3"], t["w2"], offsets=off,
+                                               stream=stream))
+
+        both = [run(k, t, off, streams[k] if i % 4 else streams[k].cuda_stream) for i, (k, t, off) in enumerate(jobs)]
+        torch.cuda.synchronize()
+        for (k, t, off), got in zip(jobs, both):
+            assert all(torch.equal(a, b) for a, b in zip(got, run(k, t, off, None)))
+        for layer in layers:
+            layer.sync_status()
+    finally:
+        for layer in layers:
+            layer.close()
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_sizes(m, seed):
+    import random
+    rng = random.Random(seed)
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))  # noqa: E731
+    dtype = rng.choice(["bf16", "bf16", "f32"])
+    n, d, F = rng.choice([1, 1, 2, 5, 9, 40]), 64 * log(1, 20), 64 * log(1, 24)
+    counts = [0 if rng.random() < 0.2 else log(1, 600 if n < 9 else 60) for _ in range(n)]
+    before, after = rng.choice([(0, 0), (1, 5)])
+    host = None if n == 1 and not before else offsets_of(counts, before)
+    R = before + sum(counts) + after
+    if host is None:
+        R = max(R, 1)
+    if R == 0:
+        return
+    t = make(n, R, d, F, dtype, seed=seed)
+    off = None if host is None else torch.tensor(host, dtype=torch.int32).cuda()
+    inside = slice(0, R) if host is None else slice(host[0], host[-1])
+    layer = m.MoELayer(n, 1, d, F, dtype)
+    try:
+        want = ref.ffn_forward(t["x"], t["w1"], t["w3"], t["w2"], host, DT[dtype])
+        got = layer.ffn_forward(t["x"], t["w1"], t["w3"], t["w2"], offsets=off, keep=True)
+        for k, v in zip(("y", "gate", "up"), got):
+            ref.check(v, want[k], inside, dtype=DT[dtype])
+        args = [t[k] for k in ("dy", "x", "gate", "up", "w1", "w3", "w2")]
+        want = ref.ffn_backward(*args, host, DT[dtype])
+        for k, v in zip(NAMES, layer.ffn_backward(*args, offsets=off)):
+            ref.check(v, want[k], inside if k == "dx" else None, dtype=DT[dtype])
+        layer.sync_status()
     finally:
         layer.close()

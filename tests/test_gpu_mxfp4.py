@@ -295,3 +295,51 @@ def test_under_a_captured_graph(m):
         layer.sync_status()
     finally:
         layer.close()
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_products(m, seed):
+    import random
+    rng = random.Random(seed)
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))  # noqa: E731
+    dtype, pair = rng.choice(["bf16", "f32"]), rng.random() < 0.4
+    n, K, N = rng.choice([1, 1, 3, 8, 30]), 32 * log(1, 90), log(1, 3000)
+    offsets = [rng.choice([0, 2])]
+    for _ in range(n):
+        offsets.append(offsets[-1] + (0 if rng.random() < 0.2 else log(1, 900 if n < 8 else 80)))
+    R = offsets[-1] + rng.choice([0, 3])
+    if offsets[-1] == offsets[0]:
+        return
+    a, w = random_mx((R, K), seed), random_mx((n, N, K), seed + 100)
+    p = random_mx((n, N, K), seed + 200) if pair else None
+    want = ref.mx_matmul(ref.mx_values(*a), ref.mx_values(*w), ref.mx_values(*p) if pair else None, offsets, DT[dtype])
+    layer = m.MoELayer(n, 1, 64, 64, dtype)
+    try:
+        out = layer.matmul_mxfp4(dev_mx(a), dev_mx(w), pair=dev_mx(p) if pair else None,
+                                 offsets=torch.tensor(offsets, dtype=torch.int32).cuda())
+        layer.sync_status()
+        ref.check(out, want, slice(offsets[0], offsets[-1]), roundings=1, dtype=DT[dtype])
+    finally:
+        layer.close()
+
+
+def test_a_graph_keeps_its_scratch_when_later_calls_need_more(m):
+    a = random_mx((30, 64), 1)
+    w, wide = dev_mx(random_mx((1, 40, 64), 2)), dev_mx(random_mx((1, 4000, 64), 3))
+    layer = m.MoELayer(1, 1, 64, 64, "bf16")
+    try:
+        x = dev_mx(a)
+        want = layer.matmul_mxfp4(x, w)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = layer.matmul_mxfp4(x, w)
+        layer.matmul_mxfp4(x, wide)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        layer.sync_status()
+    finally:
+        layer.close()
