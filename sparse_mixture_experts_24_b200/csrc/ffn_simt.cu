@@ -15,10 +15,15 @@
 // so that the pairs a, b and da, db of one hidden column meet in one thread.
 // The reduction runs in chunks of 16 through three shared-memory buffers, the
 // next two chunks' asynchronous copies in flight while one is multiplied.
+// With 3 blocks (12 warps) per SM the multiply-adds keep their pipe 68% busy (2,048 rows,
+// 1,024 x 1,024; counters), 50 TFLOP/s over 4,096 rows.
 // One warp per scheduler issues a multiply-add every other cycle at best, and
 // small batches have fewer tiles than SMs: a row product is then split along
 // its reduction over a cluster of up to 8 blocks, whose partial sums meet in
-// distributed shared memory and are added in rank order.
+// distributed shared memory and are added in rank order.  A tile of at most 32
+// rows is split over the block's own warps too.  One expert of 256 x 768, 10 rows:
+// forward 14.5 us (22.2 with whole tiles and the epilogue unrolled), backward 25.3
+// (39.2); two rows of 8 experts of 640 x 1,216: 25.8 (44.8) and 54.5 (81.2).
 #include <algorithm>
 #include <cstddef>
 
@@ -36,9 +41,8 @@ __device__ __forceinline__ const float* at(const void* p, int64_t i) { return st
 
 // Asynchronous copies into shared memory; zeros instead where `in` is false (the
 // source is not read then).
-__device__ __forceinline__ void copy4(float* dst, const float* src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0)
-                 : "memory");
+__device__ __forceinline__ void copy4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0)
@@ -63,30 +67,38 @@ __device__ __forceinline__ void store4(void* p, int64_t i, float a, float b, flo
     *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(a, b, c, d);
 }
 
+// Operands are kept as [k][position].  The weights of kFfnGrad and kFfnDx, which lie
+// along the reduction, keep that order: 16 values per column, four columns to a line
+// whose padding spreads a warp's 16-byte reads over the banks.
+constexpr int kLinesB = kN / 4, kLineB = 4 * kK + 4;
 struct Tiles {
-    float a[kBuffers][kK][kM + 4];  // rows of both arrays stay 16-byte aligned: they are read as float4
-    float b[kBuffers][kK][kN + 4];
+    float a[kBuffers][kK][kM + 4];
+    union {
+        float b[kBuffers][kK][kN + 4];
+        float bk[kBuffers][kLinesB][kLineB];
+    };
 };
 struct __align__(16) Smem {
     union {
         Tiles t;
-        float part[64][kThreads];  // a split reduction's accumulators: [value of the thread][thread]
+        float4 part[16][kThreads];  // every thread's accumulators: four columns, [2 * row + half][thread]
     };
     SegmentPlan plan;
 };
-static_assert((kM + 4) % 4 == 0 && (kN + 4) % 4 == 0 && offsetof(Tiles, b) % 16 == 0, "float4 alignment");
+static_assert((kM + 4) % 4 == 0 && (kN + 4) % 4 == 0 && kLineB % 4 == 0 && sizeof(Tiles::a) % 16 == 0,
+              "float4 alignment");
 
 }  // namespace ffn_simt
 
 using namespace ffn_simt;
 
 template <int kOp>
-__global__ void __launch_bounds__(kThreads, kOp == kFfnGrad || kOp == kFfnDx ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, 3)
     ffn_simt_kernel(const FfnArgs g, const int splits) {
     griddep_wait();
     __shared__ Smem sm;
     load_plan(sm.plan, g.offsets, g.n, g.R, kM, g.status);
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x;
     const int d = g.d, F = g.F;
 
     // the tile: expert, first output row (row ops: a row of the batch) and the
@@ -121,6 +133,11 @@ __global__ void __launch_bounds__(kThreads, kOp == kFfnGrad || kOp == kFfnDx ? 4
     const int cols = kOp == kFfnUp || kOp == kFfnGrad ? F : (kOp == kFfnDw && !dw2 ? F : d);
     const int64_t w_at = static_cast<int64_t>(e) * d * F;
     const int64_t seg0 = kOp == kFfnDw ? sm.plan.off[e] : 0;
+    // A tile of at most 16 (32) rows needs one (two) of the four warps: all four then
+    // take the same rows and a quarter (half) of every chunk each.
+    const int groups = kOp == kFfnDw || rows > 32 ? 1 : (rows > 16 ? 2 : 4);
+    const int per = kThreads / groups, group = tid / per, base = tid % per;
+    const int tx = base & 15, ty = base >> 4;
 
     // Copies of chunk c (16 of the reduction) into buffer `buf`: 16 bytes where the
     // operand lies along the tile's rows or columns, element by element where it
@@ -138,26 +155,27 @@ __global__ void __launch_bounds__(kThreads, kOp == kFfnGrad || kOp == kFfnDx ? 4
                 copy16(&sm.t.a[buf][k][m], dw2 ? at(g.h, row * F + row0 + m) : at(g.x, row * d + row0 + m), in);
             }
         } else {
-            const int k = tid & 15, ld = kOp == kFfnUp || kOp == kFfnGrad ? d : F;
-            const void* base = kOp == kFfnUp     ? g.x
-                               : kOp == kFfnDown ? g.h
-                               : kOp == kFfnGrad ? g.dy
-                                                 : (second ? g.db : g.da);
+            const int k = tid & 15, ld = kOp == kFfnGrad || kOp == kFfnUp ? d : F;
+            const void* src = kOp == kFfnUp     ? g.x
+                              : kOp == kFfnDown ? g.h
+                              : kOp == kFfnGrad ? g.dy
+                                                : (second ? g.db : g.da);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int r = (tid >> 4) + 8 * i;
-                const bool in = r < rows;
-                copy4(&sm.t.a[buf][k][r], at(base, (static_cast<int64_t>(row0) + (in ? r : 0)) * ld + k0 + k), in);
+                if (r < rows)  // a row past the last only meets its own sums
+                    copy4(&sm.t.a[buf][k][r], at(src, (static_cast<int64_t>(row0) + r) * ld + k0 + k));
             }
         }
         if (kOp == kFfnGrad || kOp == kFfnDx) {  // B(n, k): the weights' rows, k contiguous
-            const int k = tid & 15, ld = kOp == kFfnGrad ? d : F;
-            const void* base = kOp == kFfnGrad ? g.w2 : (second ? g.w3 : g.w1);
+            const int ld = kOp == kFfnGrad ? d : F;
+            const void* src = kOp == kFfnGrad ? g.w2 : (second ? g.w3 : g.w1);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int n = (tid >> 4) + 8 * i, c0 = col[0] + n;  // the halves adjoin
+            for (int i = 0; i < 4; ++i) {
+                const int p = tid + i * kThreads, n = p >> 2, k = (p & 3) * 4, c0 = col[0] + n;  // the halves adjoin
                 const bool in = c0 < cols;
-                copy4(&sm.t.b[buf][k][n], at(base, w_at + static_cast<int64_t>(in ? c0 : 0) * ld + k0 + k), in);
+                copy16(&sm.t.bk[buf][n >> 2][(n & 3) * kK + k],
+                       at(src, w_at + static_cast<int64_t>(in ? c0 : 0) * ld + k0 + k), in);
             }
         } else {  // n contiguous
 #pragma unroll
@@ -176,7 +194,12 @@ __global__ void __launch_bounds__(kThreads, kOp == kFfnGrad || kOp == kFfnDx ? 4
         }
     };
 
-    uint64_t acc2[8][4];  // two neighbouring columns each
+    // Pairs of outputs: of neighbouring columns (a row's value twice), or of neighbouring
+    // rows where B is read along the reduction (a column's value twice).  Turning B over
+    // on its way in instead takes four times the copies: as fast for many rows, slower
+    // for few (32 rows, 1,024 x 4,096, backward: 118 us against 139).
+    constexpr bool kRowPairs = kOp == kFfnGrad || kOp == kFfnDx;
+    uint64_t acc2[8][4];  // [row][column pair] or [column][row pair]
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -185,76 +208,133 @@ __global__ void __launch_bounds__(kThreads, kOp == kFfnGrad || kOp == kFfnDx ? 4
     const int rank = kOp == kFfnDw ? 0 : static_cast<int>(blockIdx.x) % splits;
     const int64_t all = (K + kK - 1) / kK, c0 = kOp == kFfnDw ? 0 : all * rank / splits;
     const int64_t chunks = kOp == kFfnDw ? all : all * (rank + 1) / splits - c0;
-    // kBuffers - 1 chunks ahead; an empty group keeps the count where there is none
+    auto multiply = [&](int buf, int kq) {  // four of the reduction
+        if (kRowPairs) {
 #pragma unroll
-    for (int i = 0; i < kBuffers - 1; ++i) {
-        if (i < chunks) issue(c0 + i, i);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    int buf = 0;
-    for (int64_t c = 0; c < chunks; ++c) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kBuffers - 2) : "memory");
-        __syncthreads();  // chunk c is there for all, and all have done with chunk c - 1
-        if (c + kBuffers - 1 < chunks) issue(c0 + c + kBuffers - 1, buf == 0 ? kBuffers - 1 : buf - 1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
+            for (int half = 0; half < 2; ++half) {
+                float4 b[4];
 #pragma unroll
-        for (int k = 0; k < kK; ++k) {
-            const float4 a0 = *reinterpret_cast<const float4*>(&sm.t.a[buf][k][ty * 8]);
-            const float4 a1 = *reinterpret_cast<const float4*>(&sm.t.a[buf][k][ty * 8 + 4]);
-            const float4 b0 = *reinterpret_cast<const float4*>(&sm.t.b[buf][k][tx * 4]);
-            const float4 b1 = *reinterpret_cast<const float4*>(&sm.t.b[buf][k][64 + tx * 4]);
-            const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-            const uint64_t bv[4] = {pair2(b0.x, b0.y), pair2(b0.z, b0.w), pair2(b1.x, b1.y), pair2(b1.z, b1.w)};
+                for (int j = 0; j < 4; ++j)
+                    b[j] = *reinterpret_cast<const float4*>(&sm.t.bk[buf][half * 16 + tx][j * kK + kq * 4]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint64_t a2 = pair2(av[i], av[i]);
+                for (int k = 0; k < 4; ++k) {
+                    const float4 a0 = *reinterpret_cast<const float4*>(&sm.t.a[buf][kq * 4 + k][ty * 8]);
+                    const float4 a1 = *reinterpret_cast<const float4*>(&sm.t.a[buf][kq * 4 + k][ty * 8 + 4]);
+                    const uint64_t av[4] = {pair2(a0.x, a0.y), pair2(a0.z, a0.w), pair2(a1.x, a1.y), pair2(a1.z, a1.w)};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) fma2(acc2[i][j], a2, bv[j]);
+                    for (int j = 0; j < 4; ++j) {
+                        const float v = k == 0 ? b[j].x : (k == 1 ? b[j].y : (k == 2 ? b[j].z : b[j].w));
+                        const uint64_t b2 = pair2(v, v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) fma2(acc2[half * 4 + j][i], av[i], b2);
+                    }
+                }
             }
+        } else {
+#pragma unroll
+            for (int k = kq * 4; k < kq * 4 + 4; ++k) {
+                const float4 a0 = *reinterpret_cast<const float4*>(&sm.t.a[buf][k][ty * 8]);
+                const float4 a1 = *reinterpret_cast<const float4*>(&sm.t.a[buf][k][ty * 8 + 4]);
+                const float4 b0 = *reinterpret_cast<const float4*>(&sm.t.b[buf][k][tx * 4]);
+                const float4 b1 = *reinterpret_cast<const float4*>(&sm.t.b[buf][k][64 + tx * 4]);
+                const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+                const uint64_t bv[4] = {pair2(b0.x, b0.y), pair2(b0.z, b0.w), pair2(b1.x, b1.y), pair2(b1.z, b1.w)};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint64_t a2 = pair2(av[i], av[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) fma2(acc2[i][j], a2, bv[j]);
+                }
+            }
+        }
+    };
+    // The copies run kBuffers - 1 chunks ahead; an empty group keeps the count where
+    // there is none.  One loop from the first copy on: each copy of this code that
+    // a block meets for the first time costs it a microsecond of instruction fetches.
+    int buf = 0, into = 0;
+    for (int64_t c = 1 - kBuffers; c < chunks; ++c) {
+        if (c >= 0) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kBuffers - 2) : "memory");
+            __syncthreads();  // chunk c is there for all, and all have done with chunk c - 1
+        }
+        if (c + kBuffers - 1 < chunks) issue(c0 + c + kBuffers - 1, into);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++into == kBuffers) into = 0;
+        if (c < 0) continue;
+        if (groups == 1) {
+#pragma unroll
+            for (int kq = 0; kq < kK / 4; ++kq) multiply(buf, kq);
+        } else {
+            for (int kq = group * (kK / 4 / groups); kq < (group + 1) * (kK / 4 / groups); ++kq) multiply(buf, kq);
         }
         if (++buf == kBuffers) buf = 0;
     }
-    __syncthreads();  // the buffers hold the partial sums next
+    __syncthreads();  // the buffers hold the sums next
 
-    float acc[8][8];
+    // The sums go through shared memory, also where nothing is added to them: the
+    // rest is then a loop over the thread's rows rather than eight copies of it.
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[i][2 * j]), "=f"(acc[i][2 * j + 1]) : "l"(acc2[i][j]));
-    if (kOp != kFfnDw && splits > 1) {
-        // rank q finishes rows i = q, q + splits, ... of every thread's eight
+        for (int h = 0; h < 2; ++h) {
+            float v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+            for (int j = 0; j < 4; ++j) {
+                const uint64_t p = kRowPairs ? acc2[4 * h + j][i >> 1] : acc2[i][2 * h + (j >> 1)];
+                float lo, hi;
+                asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+                v[j] = (kRowPairs ? i & 1 : j & 1) ? hi : lo;
+            }
+            sm.part[2 * i + h][tid] = make_float4(v[0], v[1], v[2], v[3]);
+        }
+    if (groups > 1) {  // the block's own groups first
+        __syncthreads();
+        for (int v = group * (16 / groups); v < (group + 1) * (16 / groups); ++v) {
+            float4 sum = sm.part[v][base];
+            for (int q = 1; q < groups; ++q) {
+                const float4 u = sm.part[v][base + q * per];
+                sum.x += u.x, sum.y += u.y, sum.z += u.z, sum.w += u.w;
+            }
+            sm.part[v][base] = sum;
+        }
+        if (splits == 1) __syncthreads();
+    }
+    if (splits > 1) cluster_sync();
+    const uint32_t part = smem_u32(&sm.part[0][base]);
+
+    // rank and group finish every (splits * groups)th of the thread's eight rows
+    for (int i = rank + splits * group; i < 8; i += splits * groups) {
+        const int r = ty * 8 + i;
+        if (r >= rows) break;
+        float v[8];
+        {
+            const float4 lo = sm.part[2 * i][base], hi = sm.part[2 * i + 1][base];
+            v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+            v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+        }
+        if (kOp != kFfnDw && splits > 1) {
+            float u[8][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sm.part[i * 8 + j][tid] = acc[i][j];
-        cluster_sync();
-        const uint32_t mine = smem_u32(&sm.part[0][tid]);
+            for (int q = 0; q < 8; ++q) {
+                if (q >= splits) break;
+                const uint32_t from = mapa_shared(part + 2 * i * kThreads * 16, q);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i % splits != rank) continue;
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            for (int q = 0; q < splits; ++q) {
-                const uint32_t from = mapa_shared(mine + i * 8 * kThreads * 4, q);
-                float u[8];  // eight loads in flight
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u[j]) : "r"(from + j * kThreads * 4) : "memory");
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += u[j];
+                for (int h = 0; h < 2; ++h)
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(u[q][4 * h]), "=f"(u[q][4 * h + 1]), "=f"(u[q][4 * h + 2]), "=f"(u[q][4 * h + 3])
+                                 : "r"(from + h * kThreads * 16)
+                                 : "memory");
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i][j] = v[j];
-        }
-        cluster_sync();  // the partial sums stay until every block has read them
-    }
-
+            for (int j = 0; j < 8; ++j) v[j] = u[0][j];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = ty * 8 + i;
-        if (r >= rows || (kOp != kFfnDw && i % splits != rank)) continue;
+            for (int q = 1; q < 8; ++q) {
+                if (q >= splits) break;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += u[q][j];
+            }
+        }
         const int64_t row = static_cast<int64_t>(row0) + r;
-        const float* v = acc[i];
         if (kOp == kFfnUp) {
             const int64_t at = row * F + col[0] + tx * 4;
             float h[4];
@@ -295,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, kOp == kFfnGrad || kOp == kFfnDx ? 4
             }
         }
     }
+    if (splits > 1) cluster_sync();  // the sums stay until every block has read them
     griddep_launch_dependents();
 }
 
@@ -302,7 +383,7 @@ template <int kOp>
 static cudaError_t launch_row_op(const FfnArgs& a, int column_tiles, int K, int num_sms, cudaStream_t st) {
     const int64_t blocks = (a.R + kM - 1) / kM + a.n;  // at most
     const int64_t likely = std::max<int64_t>((a.R + kM - 1) / kM, std::min<int64_t>(a.n, a.R));
-    // 3 or 4 blocks per SM run together; twice as many even out over the SMs
+    // 3 blocks per SM run together; twice as many and more even out over the SMs
     int splits = 1;
     while (splits < 8 && likely * column_tiles * splits * 2 <= 8 * num_sms && K / kK >= 8 * splits) splits *= 2;
     cudaLaunchConfig_t cfg = {};
