@@ -61,38 +61,70 @@ constexpr int smem_bytes() {
 
 __device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.f, 1.f + __expf(-a)); }
 
-__device__ __forceinline__ float load_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 load_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
-__device__ __forceinline__ void put(void* base, int64_t at, float v) {
-    static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(v);
-}
-__device__ __forceinline__ float get(const void* base, int64_t at) {
-    return bf16_bits_to_float(static_cast<const uint16_t*>(base)[at]);
+// The sum of 16 bytes at `addr` over the cluster's CTAs, in rank order, with all
+// loads in flight together.
+__device__ __forceinline__ float4 sum_cluster(uint32_t addr, int splits) {
+    float4 v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (q < splits) v[q] = load_cluster(mapa_shared(addr, q));
+#pragma unroll
+    for (int q = 1; q < 8; ++q)
+        if (q < splits) v[0].x += v[q].x, v[0].y += v[q].y, v[0].z += v[q].z, v[0].w += v[q].w;
+    return v[0];
 }
 
-// One output: weight column col, row `row` of the batch, accumulators v (and u,
-// kFfnUp).
+__device__ __forceinline__ void put4(void* base, int64_t at, const float (&v)[4]) {
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + at) =
+        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+__device__ __forceinline__ void get4(const void* base, int64_t at, float (&v)[4]) {
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + at);
+    v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+    v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+
+// Weight columns col .. col + 3 (d and ffn are multiples of 64) of row `row` of the
+// batch: accumulators v (and u, kFfnUp).
 template <int kOp>
-__device__ __forceinline__ void finish(const FfnArgs& f, int64_t row, int col, float v, float u) {
+__device__ __forceinline__ void finish4(const FfnArgs& f, int64_t row, int col, const float4& v4, const float4& u4) {
+    const float v[4] = {v4.x, v4.y, v4.z, v4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
     if (kOp == kFfnUp) {
         const int64_t at = row * f.F + col;
         if (f.gate) {
-            put(f.gate, at, v);
-            put(f.up, at, u);
+            put4(f.gate, at, v);
+            put4(f.up, at, u);
         }
-        put(f.h, at, v * sigmoid(v) * u);
+        float h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = v[j] * sigmoid(v[j]) * u[j];
+        put4(f.h, at, h);
     } else if (kOp == kFfnGrad) {
         const int64_t at = row * f.F + col;
-        const float a = get(f.gate, at), b = get(f.up, at), s = sigmoid(a), as = a * s;
-        put(f.h, at, as * b);
-        put(f.db, at, v * as);
-        put(f.da, at, v * b * (s + as * (1.f - s)));
+        float a[4], b[4], da[4], db[4], h[4];
+        get4(f.gate, at, a);
+        get4(f.up, at, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float s = sigmoid(a[j]), as = a[j] * s;
+            h[j] = as * b[j];
+            db[j] = v[j] * as;
+            da[j] = v[j] * b[j] * (s + as * (1.f - s));
+        }
+        put4(f.h, at, h);
+        put4(f.db, at, db);
+        put4(f.da, at, da);
     } else {
-        put(kOp == kFfnDown ? f.y : f.dx, row * f.d + col, v);
+        put4(kOp == kFfnDown ? f.y : f.dx, row * f.d + col, v);
     }
 }
 
@@ -229,7 +261,6 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
         // ---------------- accumulators ----------------
         const int quad = warp & 3;  // TMEM lanes 32 * quad .. + 31
         const int c = quad * 32 + lane;
-        const int cols = kOp == kFfnUp || kOp == kFfnGrad ? f.F : f.d;
         const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
         const bool done = mbar_wait(smem_u32(&tail->accum_full), 0, status, kStatusTimeoutAccum);
         __syncwarp();
@@ -245,36 +276,33 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float vf = __uint_as_float(v[i]), uf = kOp == kFfnUp ? __uint_as_float(u[i]) : 0.f;
-                    if (splits > 1) {
-                        part[(t0 + i) * kBM + c] = vf;
-                        if (kOp == kFfnUp) part[(kT + t0 + i) * kBM + c] = uf;
-                    } else if (t0 + i < rows && col0 + c < cols) {
-                        finish<kOp>(f, static_cast<int64_t>(row0) + t0 + i, col0 + c, vf, uf);
-                    }
+                    part[(t0 + i) * kBM + c] = vf;
+                    if (kOp == kFfnUp) part[(kT + t0 + i) * kBM + c] = uf;
                 }
                 __syncwarp();
             }
         }
     }
     __syncwarp();
-    if (splits > 1) {
-        // every CTA of the cluster finishes its share of the rows
+    if (splits > 1)
         cluster_sync();
+    else
+        __syncthreads();
+    {
+        // every CTA of the cluster finishes its share of the rows, a warp one at a time
         const int cols = kOp == kFfnUp || kOp == kFfnGrad ? f.F : f.d;
         const uint32_t part = smem_u32(smem);
-        if (threadIdx.x < kBM && col0 + static_cast<int>(threadIdx.x) < cols) {
-            for (int t = rank; t < rows; t += splits) {
-                float v = 0.f, u = 0.f;
-                for (int q = 0; q < splits; ++q) {
-                    v += load_cluster(mapa_shared(part + (t * kBM + threadIdx.x) * 4, q));
-                    if (kOp == kFfnUp) u += load_cluster(mapa_shared(part + ((kT + t) * kBM + threadIdx.x) * 4, q));
-                }
-                finish<kOp>(f, static_cast<int64_t>(row0) + t, col0 + static_cast<int>(threadIdx.x), v, u);
+        const int col = lane * 4;
+        if (col0 + col < cols)
+            for (int t = rank + splits * warp; t < rows; t += splits * (ffn_few::kThreads / 32)) {
+                const float4 v = sum_cluster(part + (t * kBM + col) * 4, splits);
+                const float4 u = kOp == kFfnUp ? sum_cluster(part + ((kT + t) * kBM + col) * 4, splits)
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+                finish4<kOp>(f, static_cast<int64_t>(row0) + t, col0 + col, v, u);
             }
-        }
         __syncwarp();
-        cluster_sync();  // the partial sums stay until every CTA has read them
     }
+    if (splits > 1) cluster_sync();  // the partial sums stay until every CTA has read them
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
