@@ -311,6 +311,27 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
     }
 }
 
+static int out_cols(int op, const FfnArgs& f) { return op == kFfnUp || op == kFfnGrad ? f.F : f.d; }
+static int out_steps(int op, const FfnArgs& f) {
+    return (op == kFfnUp || op == kFfnGrad ? f.d : (op == kFfnDown ? f.F : 2 * f.F)) / kBK;
+}
+// The most rows that an expert is likely to have (ragged experts: up to about 1.4
+// times the average), and the blocks of `height` rows that all of them make, rather
+// too many than too few: one more than run together costs a whole round.
+static int64_t most_rows(const FfnArgs& f) { return f.n == 1 ? f.R : (7 * f.R + 5 * f.n - 1) / (5 * f.n); }
+static int64_t likely_blocks(const FfnArgs& f, int height) {
+    const int64_t used = std::min<int64_t>(f.n, f.R);
+    if (f.n == 1) return (f.R + height - 1) / height;
+    return most_rows(f) <= height ? used : f.R / height + used;
+}
+// The reduction is split while all CTAs run together and keep 8 steps.
+static int out_splits(int op, const FfnArgs& f, int height, int num_sms) {
+    const int64_t tiles = (out_cols(op, f) + kBM - 1) / kBM * likely_blocks(f, height);
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= num_sms && out_steps(op, f) >= 8 * splits) splits *= 2;
+    return splits;
+}
+
 template <int kOp, int kT>
 static cudaError_t launch_few(const CUtensorMap* m, const FfnArgs& f, int num_sms, cudaStream_t st) {
     constexpr int smem = smem_bytes<kOp, kT>();
@@ -318,14 +339,9 @@ static cudaError_t launch_few(const CUtensorMap* m, const FfnArgs& f, int num_sm
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(ffn_few_kernel<kOp, kT>), smem, done);
     if (e != cudaSuccess) return e;
-    const int cols = kOp == kFfnUp || kOp == kFfnGrad ? f.F : f.d;
-    const int K = kOp == kFfnUp || kOp == kFfnGrad ? f.d : (kOp == kFfnDown ? f.F : 2 * f.F);
-    const int64_t tiles = (cols + kBM - 1) / kBM;
+    const int64_t tiles = (out_cols(kOp, f) + kBM - 1) / kBM;
     const int64_t blocks = (f.R + kT - 1) / kT + f.n;  // at most
-    // row blocks that are likely there: one per expert that has rows
-    const int64_t likely = std::max<int64_t>((f.R + kT - 1) / kT, std::min<int64_t>(f.n, f.R));
-    int splits = 1;
-    while (splits < 8 && tiles * likely * splits * 2 <= num_sms && K / kBK >= 8 * splits) splits *= 2;
+    const int splits = out_splits(kOp, f, kT, num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(ffn_few::kThreads);
@@ -341,7 +357,7 @@ static cudaError_t launch_few(const CUtensorMap* m, const FfnArgs& f, int num_sm
     cfg.attrs = attr;
     cfg.numAttrs = (g_chain_started && pdl_enabled()) ? 2 : 1;
     g_chain_started = true;
-    return cudaLaunchKernelEx(&cfg, ffn_few_kernel<kOp, kT>, m[0], m[1], m[2], m[3], f, K / kBK, splits);
+    return cudaLaunchKernelEx(&cfg, ffn_few_kernel<kOp, kT>, m[0], m[1], m[2], m[3], f, out_steps(kOp, f), splits);
 }
 
 template <int kT>
@@ -355,36 +371,45 @@ static cudaError_t launch_few_op(int op, const CUtensorMap* m, const FfnArgs& f,
     return cudaErrorInvalidValue;
 }
 
-// Which kernel takes a row product.  One tile of 32 or 128 rows has to hold an
-// expert's rows (ragged experts: up to about 1.4 times the average), for every
-// further tile reads the weights again.  Then this kernel is taken
-//   - where the other one's 256 x 256 tiles would leave SMs idle.  One expert of
-//     4,096 x 14,336, forward / hidden and input gradients: 16 rows 67 / 80 us
-//     against 130 / 183, 128 rows 90 / 160 against 132 / 188; 200 rows (two
-//     tiles) 151 / 260 against 133 / 189;
-//     (the hidden gradient in 128-row tiles is not: a thread's column-wise
-//     elementwise part over 128 rows costs more than the idle SMs; with the weight
-//     gradients after it, 128 rows 190 us against 122);
-//   - forward, where the reduction is long enough (48 steps) that a tile's start,
-//     which nothing overlaps here, does not count: 8 such experts, 64 rows 394
-//     against 476 us, 400 rows 478 against 523 (but backward, 128 rows, 560
-//     against 517); 128 experts of 2,048 x 768, 1,024 rows: 336 against 256;
-//   - forward, in 32-row tiles that make at most two rounds: 8 experts of 1,024 x
-//     2,816, 64 rows 41 against 47 us.
+// Which kernel takes a row product: this one in tiles of the returned rows, or
+// (0) the other one in tiles of 256 x 256 by pairs of CTAs.
+//   kFfnUp    in tiles of 32 rows wherever they hold an expert's rows (128 experts of
+//             2,048 x 768, 1,024 rows, with the output projection: 225 us against 256);
+//   kFfnDown  wherever one tile holds them and the reduction is 48 steps or longer (8
+//             experts of 4,096 x 14,336, 400 rows, the whole block: 478 against 523);
+//   else, and for the backward products, what two estimates say, in steps of 64 (about
+//             0.35 us).  A tile here takes its share of the steps (kFfnUp, two matrices:
+//             1.4 times as long) and 10 more, the other kernel's last tile 18 more;
+//             the rows' output and (kFfnGrad) elementwise part is counted by the row
+//             here and by the tile there, where the next tile's product hides half of
+//             it.  The reduction over a cluster decides most: one expert of 640 x 3,584,
+//             512 rows, backward 34 us against 58, 1,024 rows 43 against 59, 2,048 rows
+//             75 either way; 8 experts of 384 x 7,808, 2,000 rows, 123 against 157;
+//             kFfnGrad too for 128 rows, 21 against 29; kFfnUp and kFfnDown, one
+//             expert of 2,048 x 8,192, 150 rows: 46 and 38 us against 76 and 66.
 int ffn_few_rows(int op, const FfnArgs& f, int num_sms) {
     if (op == kFfnDw) return 0;
-    const int64_t used = std::min<int64_t>(f.n, f.R);
-    const int64_t most = f.n == 1 ? f.R : (7 * f.R + 5 * f.n - 1) / (5 * f.n);
-    const int rows = most <= 32 ? 32 : (most <= 128 ? 128 : 0);
-    if (rows == 0 || (op == kFfnGrad && rows == 128)) return 0;
-    const bool forward = op == kFfnUp || op == kFfnDown;
-    const int cols = op == kFfnUp || op == kFfnGrad ? f.F : f.d;
-    const int steps = (op == kFfnUp || op == kFfnGrad ? f.d : (op == kFfnDown ? f.F : 2 * f.F)) / kBK;
-    const int pair_cols = op == kFfnUp ? 128 : 256;
-    if (used * ((cols + pair_cols - 1) / pair_cols) < num_sms / 2) return rows;
-    if (forward && steps >= 48) return rows;
-    if (forward && rows == 32 && used * ((cols + kBM - 1) / kBM) <= 2 * static_cast<int64_t>(num_sms)) return rows;
-    return 0;
+    const int64_t most = most_rows(f);
+    const int height = most <= 32 ? 32 : 128;
+    const int64_t cols = out_cols(op, f), tiles = likely_blocks(f, height) * ((cols + kBM - 1) / kBM);
+    const int steps = out_steps(op, f);
+    if (op == kFfnUp && most <= 32) return 32;
+    if (op == kFfnDown && most <= height && steps >= 48) return height;
+    const int rows = static_cast<int>(std::min<int64_t>(most, height));
+    const int splits = out_splits(op, f, height, num_sms), share = steps / splits;
+    const int64_t rounds = (tiles * splits + num_sms - 1) / num_sms, pairs = num_sms / 2;
+    const int64_t pair_cols = op == kFfnUp ? 128 : 256;
+    const int64_t others = (likely_blocks(f, 256) * ((cols + pair_cols - 1) / pair_cols) + pairs - 1) / pairs;
+    int64_t here, there = others * steps + 18;
+    if (op == kFfnUp) {
+        here = rounds * (share * 7 / 5 + 10 + 20 * rows / 128);
+    } else if (op == kFfnGrad) {
+        here = rounds * (share + 20 + 15 * rows / 128) * 20 / 19;  // as good is not enough
+        there = others * (steps + 18) + 19;
+    } else {
+        here = rounds * (share + 10 + 10 * rows / 128);
+    }
+    return here < there ? height : 0;
 }
 
 cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, int num_sms, cudaStream_t st) {
