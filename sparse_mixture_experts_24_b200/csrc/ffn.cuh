@@ -67,6 +67,33 @@ __device__ __forceinline__ void load_plan(SegmentPlan& p, const int32_t* offsets
     __syncthreads();
 }
 
+// The tensor maps of kFfnDw: for every expert a copy of the given ones whose row
+// extent (dimension 1) is the end of the expert's segment, so that copies read
+// zeros past it.  Called by whole warps, each with 128 bytes of shared memory of
+// its own (128-byte aligned); warp `first` of `stride` writes its share.
+template <int kMaps>
+__device__ __forceinline__ void write_dw_maps(const CUtensorMap (&maps)[kMaps], CUtensorMap* out, void* scratch,
+                                              const SegmentPlan& plan, int n, int first, int stride) {
+    static_assert(sizeof(CUtensorMap) == 128, "32 words");
+    const int lane = threadIdx.x & 31;
+    for (int j = first; j < kMaps * n; j += stride) {
+        const int which = j / n, e = j - which * n;
+        static_cast<uint32_t*>(scratch)[lane] = reinterpret_cast<const uint32_t*>(&maps[which])[lane];
+        __syncwarp();
+        if (lane == 0)
+            asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(smem_u32(scratch)),
+                         "r"(max(1, plan.off[e + 1]))
+                         : "memory");
+        __syncwarp();
+        asm volatile(
+            "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+                reinterpret_cast<uint64_t>(out + j)),
+            "r"(smem_u32(scratch))
+            : "memory");
+        __syncwarp();
+    }
+}
+
 // Expert that owns row block `b` (b < blk[n]).
 __device__ __forceinline__ int plan_expert(const SegmentPlan& p, int n, int b) {
     int lo = 0, hi = n - 1;

@@ -171,7 +171,8 @@ bool map_out_weights(CUtensorMap* m, const void* p, int n, int rows, int cols) {
     return moe_api_detail::encode_bf16_64(m, p, 3, dims, strides, box);
 }
 
-moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t st, const char* what) {
+moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t st, const char* what,
+               const moe::FfnDwMaps& dw = {}) {
     cudaError_t e;
     if (v.bf16) {
         CUtensorMap m[4] = {};
@@ -203,8 +204,8 @@ moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t 
         else
             ok = map_out(&out.m[0], op == moe::kFfnDown ? a.y : a.dx, a.R, d);
         if (!ok) return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%s)", what);
-        e = few ? moe::launch_ffn_few(op, few, m, a, v.num_sms, st)
-                : moe::launch_ffn_tc(op, m, out, a, v.ffn->maps(), v.num_sms, st);
+        e = few ? moe::launch_ffn_few(op, few, m, a, dw, v.num_sms, st)
+                : moe::launch_ffn_tc(op, m, out, a, dw, v.num_sms, st);
     } else {
         e = moe::launch_ffn_simt(op, a, v.num_sms, st);
     }
@@ -213,16 +214,13 @@ moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t 
     return MOE_OK;
 }
 
-// The tensor maps of the weight gradients, one set per expert, on the device.
-moe_status run_maps(const HandleView& v, const moe::FfnArgs& a, cudaStream_t st) {
-    CUtensorMap m[moe::kFfnDwMaps];
-    if (!map_rows_across(&m[0], a.x, a.R, v.d) || !map_rows_across(&m[1], a.h, a.R, v.F) ||
-        !map_rows_across(&m[2], a.da, a.R, v.F) || !map_rows_across(&m[3], a.db, a.R, v.F) ||
-        !map_rows_across(&m[4], a.dy, a.R, v.d))
+// The operands of the weight gradients, whose per-expert maps kFfnGrad writes.
+moe_status dw_maps(const HandleView& v, const moe::FfnArgs& a, moe::FfnDwMaps* dw) {
+    if (!map_rows_across(&dw->m[0], a.x, a.R, v.d) || !map_rows_across(&dw->m[1], a.h, a.R, v.F) ||
+        !map_rows_across(&dw->m[2], a.da, a.R, v.F) || !map_rows_across(&dw->m[3], a.db, a.R, v.F) ||
+        !map_rows_across(&dw->m[4], a.dy, a.R, v.d))
         return failed(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (weight gradients)");
-    cudaError_t e = moe::launch_ffn_maps(m, a.offsets, v.n, a.R, v.ffn->maps(), a.status, st);
-    if (e != cudaSuccess) return cuda_failed(e, "tensor map launch");
-    *v.launches += 1;
+    dw->out = static_cast<CUtensorMap*>(v.ffn->maps());
     return MOE_OK;
 }
 
@@ -337,10 +335,11 @@ moe_status moe_ffn_backward(moe_handle* h, int64_t R, const int32_t* offsets, co
     a.dw3 = dw3;
     a.dw2 = dw2;
     moe::chain_begin();
-    if (dw1 && v.bf16) s = run_maps(v, a, st);
-    if (s == MOE_OK) s = run(v, moe::kFfnGrad, a, st, "feed-forward hidden gradient launch");
+    moe::FfnDwMaps dw = {};
+    if (dw1 && v.bf16) s = dw_maps(v, a, &dw);
+    if (s == MOE_OK) s = run(v, moe::kFfnGrad, a, st, "feed-forward hidden gradient launch", dw);
     if (s == MOE_OK && dx) s = run(v, moe::kFfnDx, a, st, "feed-forward input gradient launch");
-    if (s == MOE_OK && dw1) s = run(v, moe::kFfnDw, a, st, "feed-forward weight gradient launch");
+    if (s == MOE_OK && dw1) s = run(v, moe::kFfnDw, a, st, "feed-forward weight gradient launch", dw);
     return s == MOE_OK ? done() : s;
 }
 

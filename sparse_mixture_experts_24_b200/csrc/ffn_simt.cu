@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 
 template <int kOp>
 static cudaError_t launch_row_op(const FfnArgs& a, int column_tiles, int K, int num_sms, cudaStream_t st) {
-    const int64_t blocks = (a.R + kM - 1) / kM + a.n;  // at most
+    const int64_t blocks = a.R / kM + std::min<int64_t>(a.n, a.R);  // at most
     const int64_t likely = std::max<int64_t>((a.R + kM - 1) / kM, std::min<int64_t>(a.n, a.R));
     // 3 blocks per SM run together; twice as many and more even out over the SMs
     int splits = 1;

@@ -29,12 +29,15 @@
 // kFfnDx adds both of its products in one accumulator: K simply runs over da
 // with w1 and then db with w3.  kFfnDw does all three weight gradients in one
 // launch; its reduction runs over an expert's rows, which end anywhere, so each
-// expert has tensor maps of its own whose row extent is the segment's end
-// (ffn_maps_kernel): the copies read zeros past it, whatever lies there.
+// expert has tensor maps of its own whose row extent is the segment's end (the
+// copies read zeros past it, whatever lies there); kFfnGrad's epilogue warps write
+// them while they wait for their first accumulator.
 // Row tiles that reach past a segment's end compute rows of the next expert
 // and do not store them.
 //
 // Every wait is bounded (common.cuh); both CTAs of a pair leave together.
+#include <algorithm>
+
 #include "ffn.cuh"
 #include "kernels.h"
 
@@ -162,7 +165,8 @@ template <int kOp>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_tc_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
                   const __grid_constant__ CUtensorMap tm_b0, const __grid_constant__ CUtensorMap tm_b1,
-                  const __grid_constant__ FfnOutMaps tm_out, const FfnTcArgs args) {
+                  const __grid_constant__ FfnOutMaps tm_out, const __grid_constant__ FfnSideMaps<kOp> dw,
+                  const FfnTcArgs args) {
     constexpr bool kAMn = kOp == kFfnDw;                      // A is M-major in shared memory
     constexpr bool kBMn = kOp != kFfnGrad && kOp != kFfnDx;   // B is N-major
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -338,6 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const FfnArgs& f = args.f;
         uint8_t* block = smem + kStages * kStageBytes + (warp - 2) * (2 * kExchangeBytes);
         int turn = 0;
+        if constexpr (kOp == kFfnGrad)
+            if (dw.out)
+                write_dw_maps(dw.m, dw.out, block, plan, args.n, static_cast<int>(blockIdx.x) * kEpiWarps + warp - 2,
+                              static_cast<int>(gridDim.x) * kEpiWarps);
         // 32 columns of this warp's rows to one output: through its tensor map where
         // all 32 rows are stored, else row by row
         auto store = [&](const uint32_t* w, int which, void* out, int64_t row, int cols, int col, int valid) {
@@ -500,47 +508,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Tensor maps of the weight gradients: for every expert a copy of the five
-// given maps whose row extent (dimension 1) is the end of the expert's segment.
-struct FfnMapSet {
-    CUtensorMap m[kFfnDwMaps];
-};
-__global__ void __launch_bounds__(32 * kFfnDwMaps)
-    ffn_maps_kernel(const __grid_constant__ FfnMapSet set, const int32_t* offsets, int n, int64_t R,
-                    CUtensorMap* __restrict__ out, int* status) {
-    __shared__ __align__(128) CUtensorMap s_map[kFfnDwMaps];
-    __shared__ SegmentPlan plan;
-    griddep_wait();
-    load_plan(plan, offsets, n, R, kBM, status);
-    const int which = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x;
-    static_assert(sizeof(CUtensorMap) == 128, "32 words");
-    reinterpret_cast<uint32_t*>(&s_map[which])[lane] = reinterpret_cast<const uint32_t*>(&set.m[which])[lane];
-    __syncwarp();
-    if (lane == 0)
-        asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(
-                         smem_u32(&s_map[which])),
-                     "r"(max(1, plan.off[e + 1]))
-                     : "memory");
-    __syncwarp();
-    asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::
-                     "l"(reinterpret_cast<uint64_t>(out + static_cast<int64_t>(which) * n + e)),
-                 "r"(smem_u32(&s_map[which]))
-                 : "memory");
-    __syncthreads();
-    griddep_launch_dependents();
-}
-
-cudaError_t launch_ffn_maps(const CUtensorMap* maps5, const int32_t* offsets, int n, int64_t R, void* out,
-                            int* status, cudaStream_t st) {
-    FfnMapSet set;
-    for (int i = 0; i < kFfnDwMaps; ++i) set.m[i] = maps5[i];
-    return launch_k(ffn_maps_kernel, dim3(static_cast<unsigned>(n)), dim3(32 * kFfnDwMaps), 0, st, set, offsets, n, R,
-                    static_cast<CUtensorMap*>(out), status);
-}
-
 template <int kOp>
-static cudaError_t launch_op(const CUtensorMap* m, const FfnOutMaps& out, const FfnTcArgs& a, int64_t max_tiles, int num_sms,
-                             cudaStream_t st) {
+static cudaError_t launch_op(const CUtensorMap* m, const FfnOutMaps& out, const FfnSideMaps<kOp>& dw,
+                             const FfnTcArgs& a, int64_t max_tiles, int num_sms, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(ffn_tc_kernel<kOp>), kSmemBytes, done);
     if (e != cudaSuccess) return e;
@@ -561,17 +531,17 @@ static cudaError_t launch_op(const CUtensorMap* m, const FfnOutMaps& out, const 
     cfg.attrs = attr;
     cfg.numAttrs = (g_chain_started && pdl_enabled()) ? 2 : 1;
     g_chain_started = true;
-    return cudaLaunchKernelEx(&cfg, ffn_tc_kernel<kOp>, m[0], m[1], m[2], m[3], out, a);
+    return cudaLaunchKernelEx(&cfg, ffn_tc_kernel<kOp>, m[0], m[1], m[2], m[3], out, dw, a);
 }
 
 cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnOutMaps& out, const FfnArgs& f,
-                          const void* dw_maps, int num_sms, cudaStream_t st) {
+                          const FfnDwMaps& dw, int num_sms, cudaStream_t st) {
     FfnTcArgs a{};
     a.f = f;
     a.n = f.n;
     a.d = f.d;
     a.F = f.F;
-    a.maps = static_cast<const CUtensorMap*>(dw_maps);
+    a.maps = dw.out;
     auto up = [](int64_t v, int64_t by) { return static_cast<int>((v + by - 1) / by); };
     if (op == kFfnDw) {
         a.dw_tiles13 = up(f.d, kBM) * up(f.F, 128);
@@ -583,7 +553,7 @@ cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnOutMaps& out
         // one, 16,384 rows 426 against 453, 24,576 rows 486 against 482; 8 experts of
         // 4,096 x 14,336, 768 rows: 972 against 804.
         a.dw_run = a.dw_tiles13 + a.dw_tiles2 <= num_sms / 2 && f.R <= 192 * static_cast<int64_t>(f.n) ? 4 : 1;
-        return launch_op<kFfnDw>(maps, out, a, static_cast<int64_t>(f.n) * (a.dw_tiles13 + a.dw_tiles2), num_sms, st);
+        return launch_op<kFfnDw>(maps, out, {}, a, static_cast<int64_t>(f.n) * (a.dw_tiles13 + a.dw_tiles2), num_sms, st);
     }
     const int k = op == kFfnUp || op == kFfnGrad ? f.d : (op == kFfnDown ? f.F : 2 * f.F);
     a.steps = k / kBK;
@@ -591,12 +561,12 @@ cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnOutMaps& out
     // bands of 32 MB of A rows (the forward layer's measured budget)
     const int64_t band = (static_cast<int64_t>(32) << 20) / (static_cast<int64_t>(kBM) * k * 2);
     a.band = static_cast<int>(band < 1 ? 1 : band);
-    const int64_t tiles = ((f.R + kBM - 1) / kBM + f.n) * static_cast<int64_t>(a.n_tiles);
+    const int64_t tiles = (f.R / kBM + std::min<int64_t>(f.n, f.R)) * static_cast<int64_t>(a.n_tiles);
     switch (op) {
-        case kFfnUp: return launch_op<kFfnUp>(maps, out, a, tiles, num_sms, st);
-        case kFfnDown: return launch_op<kFfnDown>(maps, out, a, tiles, num_sms, st);
-        case kFfnGrad: return launch_op<kFfnGrad>(maps, out, a, tiles, num_sms, st);
-        case kFfnDx: return launch_op<kFfnDx>(maps, out, a, tiles, num_sms, st);
+        case kFfnUp: return launch_op<kFfnUp>(maps, out, {}, a, tiles, num_sms, st);
+        case kFfnDown: return launch_op<kFfnDown>(maps, out, {}, a, tiles, num_sms, st);
+        case kFfnGrad: return launch_op<kFfnGrad>(maps, out, dw, a, tiles, num_sms, st);
+        case kFfnDx: return launch_op<kFfnDx>(maps, out, {}, a, tiles, num_sms, st);
     }
     return cudaErrorInvalidValue;
 }

@@ -45,7 +45,8 @@ struct Cfg {
     static_assert(kMats * kT * kBM * 4 <= kStages * kStageBytes, "partial sums");
 };
 
-struct __align__(16) Tail {
+struct __align__(128) Tail {
+    CUtensorMap map[4];  // kFfnGrad: a map under construction per epilogue warp
     uint64_t full[kMaxStages];
     uint64_t empty[kMaxStages];
     uint64_t accum_full;
@@ -136,7 +137,7 @@ template <int kOp, int kT>
 __global__ void __launch_bounds__(ffn_few::kThreads, 1)
     ffn_few_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
                    const __grid_constant__ CUtensorMap tm_b0, const __grid_constant__ CUtensorMap tm_b1,
-                   const FfnArgs f, const int steps, const int splits) {
+                   const __grid_constant__ FfnSideMaps<kOp> dw, const FfnArgs f, const int steps, const int splits) {
     using C = Cfg<kOp, kT>;
     constexpr bool kWMn = kOp == kFfnUp || kOp == kFfnDown;  // the weights are M-major
     extern __shared__ uint8_t smem_raw[];
@@ -148,9 +149,19 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
     load_plan(tail->plan, f.offsets, f.n, f.R, kT, f.status);
     const SegmentPlan& plan = tail->plan;
     griddep_launch_dependents();
+    // the tensor maps of kFfnDw are written by warps 2 .. 5 of all CTAs
+    auto write_maps = [&]() {
+        if constexpr (kOp == kFfnGrad) {
+            if (dw.out && warp >= 2)
+                write_dw_maps(dw.m, dw.out, &tail->map[warp - 2], plan, f.n,
+                              static_cast<int>(blockIdx.y * gridDim.x + blockIdx.x) * 4 + warp - 2,
+                              static_cast<int>(gridDim.x * gridDim.y) * 4);
+        }
+    };
     // x: weight column tile and, fastest, the split of its reduction; y: row block
     if (static_cast<int>(blockIdx.y) >= plan.blk[f.n]) {
         griddep_wait();
+        write_maps();
         return;  // the whole cluster: its CTAs share blockIdx.y
     }
     const int rank = static_cast<int>(blockIdx.x) % splits, tile = static_cast<int>(blockIdx.x) / splits;
@@ -262,6 +273,10 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
         const int quad = warp & 3;  // TMEM lanes 32 * quad .. + 31
         const int c = quad * 32 + lane;
         const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+        if (kOp == kFfnGrad) {
+            griddep_wait();
+            write_maps();
+        }
         const bool done = mbar_wait(smem_u32(&tail->accum_full), 0, status, kStatusTimeoutAccum);
         __syncwarp();
         tc_fence_after();
@@ -333,14 +348,15 @@ static int out_splits(int op, const FfnArgs& f, int height, int num_sms) {
 }
 
 template <int kOp, int kT>
-static cudaError_t launch_few(const CUtensorMap* m, const FfnArgs& f, int num_sms, cudaStream_t st) {
+static cudaError_t launch_few(const CUtensorMap* m, const FfnArgs& f, const FfnSideMaps<kOp>& dw, int num_sms,
+                              cudaStream_t st) {
     constexpr int smem = smem_bytes<kOp, kT>();
     static_assert(smem <= 232448, "shared memory");
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(ffn_few_kernel<kOp, kT>), smem, done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (out_cols(kOp, f) + kBM - 1) / kBM;
-    const int64_t blocks = (f.R + kT - 1) / kT + f.n;  // at most
+    const int64_t blocks = f.R / kT + std::min<int64_t>(f.n, f.R);  // at most
     const int splits = out_splits(kOp, f, kT, num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), static_cast<unsigned>(blocks));
@@ -357,16 +373,17 @@ static cudaError_t launch_few(const CUtensorMap* m, const FfnArgs& f, int num_sm
     cfg.attrs = attr;
     cfg.numAttrs = (g_chain_started && pdl_enabled()) ? 2 : 1;
     g_chain_started = true;
-    return cudaLaunchKernelEx(&cfg, ffn_few_kernel<kOp, kT>, m[0], m[1], m[2], m[3], f, out_steps(kOp, f), splits);
+    return cudaLaunchKernelEx(&cfg, ffn_few_kernel<kOp, kT>, m[0], m[1], m[2], m[3], dw, f, out_steps(kOp, f), splits);
 }
 
 template <int kT>
-static cudaError_t launch_few_op(int op, const CUtensorMap* m, const FfnArgs& f, int num_sms, cudaStream_t st) {
+static cudaError_t launch_few_op(int op, const CUtensorMap* m, const FfnArgs& f, const FfnDwMaps& dw, int num_sms,
+                                 cudaStream_t st) {
     switch (op) {
-        case kFfnUp: return launch_few<kFfnUp, kT>(m, f, num_sms, st);
-        case kFfnDown: return launch_few<kFfnDown, kT>(m, f, num_sms, st);
-        case kFfnGrad: return launch_few<kFfnGrad, kT>(m, f, num_sms, st);
-        case kFfnDx: return launch_few<kFfnDx, kT>(m, f, num_sms, st);
+        case kFfnUp: return launch_few<kFfnUp, kT>(m, f, {}, num_sms, st);
+        case kFfnDown: return launch_few<kFfnDown, kT>(m, f, {}, num_sms, st);
+        case kFfnGrad: return launch_few<kFfnGrad, kT>(m, f, dw, num_sms, st);
+        case kFfnDx: return launch_few<kFfnDx, kT>(m, f, {}, num_sms, st);
     }
     return cudaErrorInvalidValue;
 }
@@ -412,8 +429,10 @@ int ffn_few_rows(int op, const FfnArgs& f, int num_sms) {
     return here < there ? height : 0;
 }
 
-cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, int num_sms, cudaStream_t st) {
-    return rows == 32 ? launch_few_op<32>(op, maps, f, num_sms, st) : launch_few_op<128>(op, maps, f, num_sms, st);
+cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, const FfnDwMaps& dw,
+                           int num_sms, cudaStream_t st) {
+    return rows == 32 ? launch_few_op<32>(op, maps, f, dw, num_sms, st)
+                      : launch_few_op<128>(op, maps, f, dw, num_sms, st);
 }
 
 }  // namespace moe

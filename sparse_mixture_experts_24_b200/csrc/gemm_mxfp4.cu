@@ -829,7 +829,7 @@ MxChunks mx_gemm_chunks(const MxGemmArgs& a, int num_sms) {
         ch.tile_rows = a.R <= 48 * static_cast<int64_t>(a.n) ? 64 : 128;
     const int halves = ch.tile_rows == kPairRows ? 2 : 1;
     ch.steps = (a.K + kBK - 1) / kBK;
-    ch.a_blocks = static_cast<int>(halves * ((a.R + ch.tile_rows - 1) / ch.tile_rows + a.n));
+    ch.a_blocks = static_cast<int>(halves * (a.R / ch.tile_rows + std::min<int64_t>(a.n, a.R)));
     ch.col_blocks = (a.N + 127) / 128;
     ch.blocks = ch.a_blocks + static_cast<int64_t>(a.n) * ch.col_blocks * (a.b2_codes ? 2 : 1);
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.a_scales) | reinterpret_cast<uintptr_t>(a.b_scales) |
@@ -872,7 +872,7 @@ static cudaError_t launch(const CUtensorMap* m, const MxGemmArgs& a, const MxChu
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(mx_gemm_kernel<kPair, kBf16Out, kBN, kTM>), smem, done);
     if (e != cudaSuccess) return e;
     const int64_t n_tiles = (a.N + (kPair ? 128 : kBN) - 1) / (kPair ? 128 : kBN);
-    int64_t g = ((a.R + kTM - 1) / kTM + a.n) * n_tiles;
+    int64_t g = (a.R / kTM + std::min<int64_t>(a.n, a.R)) * n_tiles;
     if (g > num_sms) g = num_sms;
     return launch_k(mx_gemm_kernel<kPair, kBf16Out, kBN, kTM>, dim3(static_cast<unsigned>(g)), dim3(kThreads), smem,
                     st, m[0], m[1], m[2], m[4], a, ch);

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 namespace moe {
 
@@ -404,10 +405,18 @@ cudaError_t launch_ffn_simt(int op, const FfnArgs& a, int num_sms, cudaStream_t 
 // ([n][K][N], kFfnUp and kFfnDown) as 4-D maps (64 columns, rows, 64-column
 // chunk, expert) in boxes of 64 rows and two chunks; weights that are K-major
 // ([n][N][K], kFfnGrad and kFfnDx) as 3-D maps in 64 x 128 boxes.  kFfnDw
-// takes its operands from the maps that launch_ffn_maps has written to device
-// memory: [5][n], of x, h, da, db, dy as 3-D maps (64 columns, rows, 64-column
-// chunk) in boxes of 64 rows and two chunks.
+// takes its operands from the maps that kFfnGrad has written to device memory:
+// [5][n], of x, h, da, db, dy as 3-D maps (64 columns, rows, 64-column chunk) in
+// boxes of 64 rows and two chunks.
 constexpr int kFfnDwMaps = 5;
+// The maps of whole operands that kFfnGrad writes [5][n] of to `out` (null: none).
+struct FfnDwMaps {
+    CUtensorMap m[kFfnDwMaps];
+    CUtensorMap* out;
+};
+struct FfnNoMaps {};
+template <int kOp>
+using FfnSideMaps = std::conditional_t<kOp == kFfnGrad, FfnDwMaps, FfnNoMaps>;
 struct FfnTcArgs {
     FfnArgs f;
     int n, d, F;
@@ -418,20 +427,19 @@ struct FfnTcArgs {
     int dw_run;   // consecutive kFfnDw tiles that one CTA pair takes
     const CUtensorMap* maps;
 };
-cudaError_t launch_ffn_maps(const CUtensorMap* maps5, const int32_t* offsets, int n, int64_t R, void* out,
-                            int* status, cudaStream_t st);
 // The row ops for few rows per expert (gemm_ffn_few.cu): ffn_few_rows gives the
 // batch rows of its tiles (the box of the row operands' maps), or 0 where
 // launch_ffn_tc is to be taken.  The weights' maps are the same.
 int ffn_few_rows(int op, const FfnArgs& f, int num_sms);
-cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, int num_sms, cudaStream_t st);
+cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, const FfnDwMaps& dw,
+                           int num_sms, cudaStream_t st);
 // Output maps in 32 x 32 boxes with 64-byte swizzle: kFfnUp h, gate, up; kFfnDown
 // y; kFfnGrad da, db, h; kFfnDx dx; kFfnDw dw1, dw3, dw2 (3-D: column, row, expert).
 struct FfnOutMaps {
     CUtensorMap m[3];
 };
 cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnOutMaps& out, const FfnArgs& f,
-                          const void* dw_maps, int num_sms, cudaStream_t st);
+                          const FfnDwMaps& dw, int num_sms, cudaStream_t st);
 
 // MXFP4 (mxfp4.cu): codes [..][K/2] and E8M0 scales [..][K/32], blocks of 32
 // along K; values (the type of the source), if given, receives what they stand

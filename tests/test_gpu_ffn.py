@@ -50,6 +50,10 @@ SHAPES = [
     (1, None, 2, 0, 0, 64, 4096),
     (2, [40, 3], 43, 0, 2, 1024, 704),
     (3, [90, 0, 131], 221, 4, 0, 576, 1088),
+    (2, [150, 300], 450, 1, 2, 640, 1792),
+    (1, None, 276, 0, 0, 640, 3584),
+    # fp32 tiles of 16, 32 and more rows, split over the block's warps
+    (4, [17, 33, 16, 49], 115, 0, 1, 256, 512),
     # more tiles than SMs: every CTA pair runs several, through both accumulators
     (3, [700, 0, 1001], 1701, 0, 3, 1024, 2112),
 ]
