@@ -94,6 +94,12 @@ __device__ __forceinline__ void write_dw_maps(const CUtensorMap (&maps)[kMaps], 
     }
 }
 
+// Before a copy by a map that the device wrote.
+__device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map))
+                 : "memory");
+}
+
 // Expert that owns row block `b` (b < blk[n]).
 __device__ __forceinline__ int plan_expert(const SegmentPlan& p, int n, int b) {
     int lo = 0, hi = n - 1;

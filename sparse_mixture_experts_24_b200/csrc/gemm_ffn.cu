@@ -146,11 +146,6 @@ __device__ __forceinline__ void hand_back_to(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
-__device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
-    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map))
-                 : "memory");
-}
-
 // 32 accumulators as 16 words of bf16 pairs.
 __device__ __forceinline__ void pack32(const uint32_t (&v)[32], uint32_t (&w)[16]) {
 #pragma unroll
@@ -224,13 +219,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = static_cast<int>(rank);
             for (int i = 0, t = cid * run; t < total && ok; t = tile_index(++i)) {
                 const Tile ti = tile_at<kOp>(t, plan, args);
-                if (kOp == kFfnDw && ti.steps > 0 && held != 2 * ti.e + (ti.dw2 ? 1 : 0)) {
-                    held = 2 * ti.e + (ti.dw2 ? 1 : 0);
-                    // maps [5][n]: x, h, da, db, dy; the peer's columns are db's
-                    ma = args.maps + (ti.dw2 ? 1 : 0) * args.n + ti.e;
-                    mb = args.maps + (ti.dw2 ? 4 : 2 + r) * args.n + ti.e;
-                    acquire_map(ma);
-                    acquire_map(mb);
+                if constexpr (kOp == kFfnDw) {
+                    if (ti.steps > 0 && held != 2 * ti.e + (ti.dw2 ? 1 : 0)) {
+                        held = 2 * ti.e + (ti.dw2 ? 1 : 0);
+                        // maps [5][n]: x, h, da, db, dy; the peer's columns are db's
+                        ma = dw.maps + (ti.dw2 ? 1 : 0) * args.n + ti.e;
+                        mb = dw.maps + (ti.dw2 ? 4 : 2 + r) * args.n + ti.e;
+                        acquire_map(ma);
+                        acquire_map(mb);
+                    }
                 }
                 for (int kb = 0; kb < ti.steps; ++kb) {
                     if (!mbar_wait(smem_u32(&tail->empty[stage]), phase ^ 1u, status, kStatusTimeoutEmpty)) {
@@ -541,7 +538,6 @@ cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnOutMaps& out
     a.n = f.n;
     a.d = f.d;
     a.F = f.F;
-    a.maps = dw.out;
     auto up = [](int64_t v, int64_t by) { return static_cast<int>((v + by - 1) / by); };
     if (op == kFfnDw) {
         a.dw_tiles13 = up(f.d, kBM) * up(f.F, 128);
@@ -553,7 +549,7 @@ cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnOutMaps& out
         // one, 16,384 rows 426 against 453, 24,576 rows 486 against 482; 8 experts of
         // 4,096 x 14,336, 768 rows: 972 against 804.
         a.dw_run = a.dw_tiles13 + a.dw_tiles2 <= num_sms / 2 && f.R <= 192 * static_cast<int64_t>(f.n) ? 4 : 1;
-        return launch_op<kFfnDw>(maps, out, {}, a, static_cast<int64_t>(f.n) * (a.dw_tiles13 + a.dw_tiles2), num_sms, st);
+        return launch_op<kFfnDw>(maps, out, {dw.out}, a, static_cast<int64_t>(f.n) * (a.dw_tiles13 + a.dw_tiles2), num_sms, st);
     }
     const int k = op == kFfnUp || op == kFfnGrad ? f.d : (op == kFfnDown ? f.F : 2 * f.F);
     a.steps = k / kBK;

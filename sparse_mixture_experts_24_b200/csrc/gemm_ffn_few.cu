@@ -1,21 +1,26 @@
-// gemm_ffn_few.cu -- the row products of the gated feed-forward block
-// (gemm_ffn.cu: kFfnUp, kFfnDown, kFfnGrad, kFfnDx) in bf16 for few rows per
-// expert, where the call is bound by reading the weights once.
+// gemm_ffn_few.cu -- the products of the gated feed-forward block (gemm_ffn.cu) in
+// bf16 where its 256 x 256 tiles would be too few or mostly empty: few rows per
+// expert, where the call is bound by reading the weights once, and outputs so
+// narrow that the reduction has to be shared out.
 //
-// The product is turned over: 128 weight columns are the MMA's M and kT rows of
-// the batch its N, so a tile needs no padding to 256 rows and there are enough
-// tiles to keep all SMs loading; where there are not (one dense expert's
-// 14,336 x 4,096 output projection has 32), the reduction is split over a
-// cluster of up to 8 CTAs, whose partial sums meet in distributed shared
-// memory, added in rank order.  Both operands keep their layouts: the weights
-// are M-major for kFfnUp and kFfnDown (their rows are the reduction) and
-// K-major for the other two, the rows are K-major.
+// The row products (kFfnUp, kFfnDown, kFfnGrad, kFfnDx) are turned over: 128 weight
+// columns are the MMA's M and kT rows of the batch its N, so a tile needs no
+// padding to 256 rows and there are enough tiles to keep all SMs loading; where
+// there are not (one dense expert's 14,336 x 4,096 output projection has 32), the
+// reduction is split over a cluster of up to 8 CTAs, whose partial sums meet in
+// distributed shared memory, added in rank order.  Both operands keep their
+// layouts: the weights are M-major for kFfnUp and kFfnDown (their rows are the
+// reduction) and K-major for the other two, the rows are K-major.  kFfnDw takes 128
+// x 128 outputs the same way, da, db or dy M-major and x or h N-major, over the
+// expert's rows.
 //
 // 192 threads, one CTA per SM (the ring takes its shared memory):
 //   warp 0     TMA, 64 of K per step: 128 weight columns (kFfnUp: of both
 //              matrices) and kT rows;
 //   warp 1     tcgen05.mma M 128, N kT, K 16 (kFfnUp: two accumulators);
-//   warps 2-5  epilogue: a thread holds one weight column of every row.
+//   warps 2-5  bring the accumulators to shared memory, one column per thread;
+//              then every warp finishes whole rows, 4 columns per lane (128 rows of
+//              1,024 x 4,096: forward 36 us when a thread kept its column, 24 so).
 // The weights do not depend on the kernel before: their copies for the whole
 // ring start before the programmatic-launch wait, under its last tiles.
 // Every wait is bounded (common.cuh).
@@ -42,6 +47,7 @@ struct Cfg {
     static constexpr int kStages = kRingBytes / kStageBytes < kMaxStages ? kRingBytes / kStageBytes : kMaxStages;
     static constexpr int kTmemCols = kMats * kT < 32 ? 32 : kMats * kT;
     // the ring holds the partial sums of a split reduction afterwards
+    static_assert(kOp != kFfnDw || kT == kBM, "two blocks of 128 columns");
     static_assert(kMats * kT * kBM * 4 <= kStages * kStageBytes, "partial sums");
 };
 
@@ -139,7 +145,8 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
                    const __grid_constant__ CUtensorMap tm_b0, const __grid_constant__ CUtensorMap tm_b1,
                    const __grid_constant__ FfnSideMaps<kOp> dw, const FfnArgs f, const int steps, const int splits) {
     using C = Cfg<kOp, kT>;
-    constexpr bool kWMn = kOp == kFfnUp || kOp == kFfnDown;  // the weights are M-major
+    constexpr bool kWMn = kOp == kFfnUp || kOp == kFfnDown || kOp == kFfnDw;  // the MMA's A is M-major
+    constexpr bool kRMn = kOp == kFfnDw;                                      // and its B N-major
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -159,18 +166,31 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
         }
     };
     // x: weight column tile and, fastest, the split of its reduction; y: row block
-    if (static_cast<int>(blockIdx.y) >= plan.blk[f.n]) {
+    if (kOp != kFfnDw && static_cast<int>(blockIdx.y) >= plan.blk[f.n]) {
         griddep_wait();
         write_maps();
         return;  // the whole cluster: its CTAs share blockIdx.y
     }
     const int rank = static_cast<int>(blockIdx.x) % splits, tile = static_cast<int>(blockIdx.x) / splits;
-    const int e = plan_expert(plan, f.n, blockIdx.y);
-    const int row0 = plan.off[e] + (static_cast<int>(blockIdx.y) - plan.blk[e]) * kT;
-    const int rows = min(kT, plan.off[e + 1] - row0);
-    const int col0 = tile * kBM;
-    const int k0 = static_cast<int>(static_cast<int64_t>(steps) * rank / splits);
-    const int k1 = static_cast<int>(static_cast<int64_t>(steps) * (rank + 1) / splits);
+    // row0, rows: the tile's rows of the batch, or (kFfnDw) of the weight gradient
+    int e, row0, rows, col0, which = 0, reduce = steps;
+    if (kOp == kFfnDw) {  // y: expert; x: dw1, dw3, dw2, as many tiles each
+        e = blockIdx.y;
+        const int nf = (f.F + kBM - 1) / kBM, nd = (f.d + kBM - 1) / kBM;
+        which = tile / (nf * nd);
+        const int local = tile - which * nf * nd, nc = which == 2 ? nd : nf;
+        row0 = local / nc * kT;
+        col0 = (local - local / nc * nc) * kBM;
+        rows = min(kT, (which == 2 ? f.F : f.d) - row0);
+        reduce = (plan.off[e + 1] - plan.off[e] + kBK - 1) / kBK;
+    } else {
+        e = plan_expert(plan, f.n, blockIdx.y);
+        row0 = plan.off[e] + (static_cast<int>(blockIdx.y) - plan.blk[e]) * kT;
+        rows = min(kT, plan.off[e + 1] - row0);
+        col0 = tile * kBM;
+    }
+    const int k0 = static_cast<int>(static_cast<int64_t>(reduce) * rank / splits);
+    const int k1 = static_cast<int>(static_cast<int64_t>(reduce) * (rank + 1) / splits);
     int* status = f.status;
 
     if (threadIdx.x == 0) {
@@ -194,6 +214,14 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             // ---------------- TMA ----------------
+            const CUtensorMap *ma = nullptr, *mb = nullptr;
+            if constexpr (kOp == kFfnDw) {  // maps [5][n]: x, h, da, db, dy
+                griddep_wait();
+                ma = dw.maps + (which == 2 ? 4 : 2 + which) * f.n + e;
+                mb = dw.maps + (which == 2 ? 1 : 0) * f.n + e;
+                acquire_map(ma);
+                acquire_map(mb);
+            }
             auto weights = [&](int kb, int stage) {
                 const uint32_t fb = smem_u32(&tail->full[stage]);
                 mbar_arrive_expect_tx(fb, C::kStageBytes);
@@ -206,6 +234,8 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
                     tma_load_4d(dst, &tm_b0, fb, 0, k, tile * 2, e);
                 } else if (kOp == kFfnGrad) {
                     tma_load_3d(dst, &tm_b0, fb, k, col0, e);
+                } else if (kOp == kFfnDw) {
+                    tma_load_3d(dst, ma, fb, 0, plan.off[e] + k, col0 / 64);
                 } else {
                     const bool second = k >= f.F;
                     tma_load_3d(dst, second ? &tm_b1 : &tm_b0, fb, second ? k - f.F : k, col0, e);
@@ -215,6 +245,10 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
                 const uint32_t fb = smem_u32(&tail->full[stage]);
                 const uint32_t dst = smem_u32(smem + stage * C::kStageBytes) + C::kMats * kWBytes;
                 const int k = kb * kBK;
+                if (kOp == kFfnDw) {
+                    tma_load_3d(dst, mb, fb, 0, plan.off[e] + k, row0 / 64);
+                    return;
+                }
                 const bool second = kOp == kFfnDx && k >= f.F;
                 tma_load_2d(dst, second ? &tm_a1 : &tm_a0, fb, second ? k - f.F : k, row0);
             };
@@ -240,7 +274,7 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
     } else if (warp == 1) {
         if (lane == 0) {
             // ---------------- MMA ----------------
-            constexpr uint32_t idesc = make_idesc_bf16(kBM, kT, kWMn ? 1 : 0, 0);
+            constexpr uint32_t idesc = make_idesc_bf16(kBM, kT, kWMn ? 1 : 0, kRMn ? 1 : 0);
             bool ok = true;
             for (int i = 0; i < k1 - k0; ++i) {
                 const int stage = i % C::kStages;
@@ -253,7 +287,9 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
                 const uint32_t base = smem_u32(smem + stage * C::kStageBytes);
 #pragma unroll
                 for (int kk = 0; kk < kBK / 16; ++kk) {
-                    const uint64_t bd = make_smem_desc(base + C::kMats * kWBytes + kk * 32, 16, 1024, 2);
+                    const uint32_t b = base + C::kMats * kWBytes;
+                    const uint64_t bd = kRMn ? make_smem_desc(b + kk * 2048, kChunk, 1024, 2)
+                                             : make_smem_desc(b + kk * 32, 16, 1024, 2);
 #pragma unroll
                     for (int m = 0; m < C::kMats; ++m) {
                         const uint32_t a = base + m * kWBytes;
@@ -290,7 +326,8 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float vf = __uint_as_float(v[i]), uf = kOp == kFfnUp ? __uint_as_float(u[i]) : 0.f;
+                    // (kFfnDw: a share, or an expert, without rows multiplies nothing)
+                    const float vf = kOp == kFfnDw && k0 == k1 ? 0.f : __uint_as_float(v[i]), uf = kOp == kFfnUp ? __uint_as_float(u[i]) : 0.f;
                     part[(t0 + i) * kBM + c] = vf;
                     if (kOp == kFfnUp) part[(kT + t0 + i) * kBM + c] = uf;
                 }
@@ -305,7 +342,7 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
         __syncthreads();
     {
         // every CTA of the cluster finishes its share of the rows, a warp one at a time
-        const int cols = kOp == kFfnUp || kOp == kFfnGrad ? f.F : f.d;
+        const int cols = kOp == kFfnUp || kOp == kFfnGrad || (kOp == kFfnDw && which != 2) ? f.F : f.d;
         const uint32_t part = smem_u32(smem);
         const int col = lane * 4;
         if (col0 + col < cols)
@@ -313,7 +350,13 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
                 const float4 v = sum_cluster(part + (t * kBM + col) * 4, splits);
                 const float4 u = kOp == kFfnUp ? sum_cluster(part + ((kT + t) * kBM + col) * 4, splits)
                                                : make_float4(0.f, 0.f, 0.f, 0.f);
-                finish4<kOp>(f, static_cast<int64_t>(row0) + t, col0 + col, v, u);
+                if (kOp == kFfnDw) {
+                    const float out[4] = {v.x, v.y, v.z, v.w};
+                    put4(which == 0 ? f.dw1 : (which == 1 ? f.dw3 : f.dw2),
+                         static_cast<int64_t>(e) * f.d * f.F + static_cast<int64_t>(row0 + t) * cols + col0 + col, out);
+                } else {
+                    finish4<kOp>(f, static_cast<int64_t>(row0) + t, col0 + col, v, u);
+                }
             }
         __syncwarp();
     }
@@ -326,10 +369,6 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
     }
 }
 
-static int out_cols(int op, const FfnArgs& f) { return op == kFfnUp || op == kFfnGrad ? f.F : f.d; }
-static int out_steps(int op, const FfnArgs& f) {
-    return (op == kFfnUp || op == kFfnGrad ? f.d : (op == kFfnDown ? f.F : 2 * f.F)) / kBK;
-}
 // The most rows that an expert is likely to have (ragged experts: up to about 1.4
 // times the average), and the blocks of `height` rows that all of them make, rather
 // too many than too few: one more than run together costs a whole round.
@@ -339,9 +378,18 @@ static int64_t likely_blocks(const FfnArgs& f, int height) {
     if (f.n == 1) return (f.R + height - 1) / height;
     return most_rows(f) <= height ? used : f.R / height + used;
 }
+static int out_cols(int op, const FfnArgs& f) { return op == kFfnUp || op == kFfnGrad ? f.F : f.d; }
+static int out_steps(int op, const FfnArgs& f) {
+    if (op == kFfnDw) return static_cast<int>(std::max<int64_t>(1, most_rows(f) / kBK));
+    return (op == kFfnUp || op == kFfnGrad ? f.d : (op == kFfnDown ? f.F : 2 * f.F)) / kBK;
+}
+static int64_t out_tiles(int op, const FfnArgs& f, int height) {
+    if (op == kFfnDw) return static_cast<int64_t>(f.n) * 3 * ((f.d + kBM - 1) / kBM) * ((f.F + kBM - 1) / kBM);
+    return (out_cols(op, f) + kBM - 1) / kBM * likely_blocks(f, height);
+}
 // The reduction is split while all CTAs run together and keep 8 steps.
 static int out_splits(int op, const FfnArgs& f, int height, int num_sms) {
-    const int64_t tiles = (out_cols(op, f) + kBM - 1) / kBM * likely_blocks(f, height);
+    const int64_t tiles = out_tiles(op, f, height);
     int splits = 1;
     while (splits < 8 && tiles * splits * 2 <= num_sms && out_steps(op, f) >= 8 * splits) splits *= 2;
     return splits;
@@ -355,8 +403,8 @@ static cudaError_t launch_few(const CUtensorMap* m, const FfnArgs& f, const FfnS
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(ffn_few_kernel<kOp, kT>), smem, done);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (out_cols(kOp, f) + kBM - 1) / kBM;
-    const int64_t blocks = f.R / kT + std::min<int64_t>(f.n, f.R);  // at most
+    const int64_t tiles = kOp == kFfnDw ? out_tiles(kOp, f, kT) / f.n : (out_cols(kOp, f) + kBM - 1) / kBM;
+    const int64_t blocks = kOp == kFfnDw ? f.n : f.R / kT + std::min<int64_t>(f.n, f.R);  // at most
     const int splits = out_splits(kOp, f, kT, num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits), static_cast<unsigned>(blocks));
@@ -404,11 +452,20 @@ static cudaError_t launch_few_op(int op, const CUtensorMap* m, const FfnArgs& f,
 //             75 either way; 8 experts of 384 x 7,808, 2,000 rows, 123 against 157;
 //             kFfnGrad too for 128 rows, 21 against 29; kFfnUp and kFfnDown, one
 //             expert of 2,048 x 8,192, 150 rows: 46 and 38 us against 76 and 66.
+//   kFfnDw    the same, a tile here costing a tenth more per step and 14: one expert of
+//             256 x 512, 8,192 rows, with the hidden gradient 34 us against 61; 640 x
+//             448, 8,021 rows, 48 against 63; 1 row of the first 13 against 16.
 int ffn_few_rows(int op, const FfnArgs& f, int num_sms) {
-    if (op == kFfnDw) return 0;
+    if (op == kFfnDw) {
+        const int steps = out_steps(op, f), splits = out_splits(op, f, 128, num_sms);
+        const int64_t rounds = (out_tiles(op, f, 128) * splits + num_sms - 1) / num_sms, pairs = num_sms / 2;
+        const int64_t d2 = (f.d + 255) / 256, F2 = (f.F + 255) / 256;
+        const int64_t others = (f.n * (d2 * ((f.F + 127) / 128) + F2 * d2) + pairs - 1) / pairs;
+        return rounds * (steps / splits * 11 / 10 + 14) < others * steps + 18 ? 128 : 0;
+    }
     const int64_t most = most_rows(f);
     const int height = most <= 32 ? 32 : 128;
-    const int64_t cols = out_cols(op, f), tiles = likely_blocks(f, height) * ((cols + kBM - 1) / kBM);
+    const int64_t cols = out_cols(op, f), tiles = out_tiles(op, f, height);
     const int steps = out_steps(op, f);
     if (op == kFfnUp && most <= 32) return 32;
     if (op == kFfnDown && most <= height && steps >= 48) return height;
@@ -431,6 +488,7 @@ int ffn_few_rows(int op, const FfnArgs& f, int num_sms) {
 
 cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, const FfnDwMaps& dw,
                            int num_sms, cudaStream_t st) {
+    if (op == kFfnDw) return launch_few<kFfnDw, 128>(maps, f, {dw.out}, num_sms, st);
     return rows == 32 ? launch_few_op<32>(op, maps, f, dw, num_sms, st)
                       : launch_few_op<128>(op, maps, f, dw, num_sms, st);
 }

@@ -414,9 +414,12 @@ struct FfnDwMaps {
     CUtensorMap m[kFfnDwMaps];
     CUtensorMap* out;
 };
-struct FfnNoMaps {};
+// What kFfnDw is given of them, and every other op.
+struct FfnReadMaps {
+    const CUtensorMap* maps;
+};
 template <int kOp>
-using FfnSideMaps = std::conditional_t<kOp == kFfnGrad, FfnDwMaps, FfnNoMaps>;
+using FfnSideMaps = std::conditional_t<kOp == kFfnGrad, FfnDwMaps, FfnReadMaps>;
 struct FfnTcArgs {
     FfnArgs f;
     int n, d, F;
@@ -425,11 +428,11 @@ struct FfnTcArgs {
     int band;     // row blocks per band of the tile order
     int dw_tiles13, dw_tiles2;
     int dw_run;   // consecutive kFfnDw tiles that one CTA pair takes
-    const CUtensorMap* maps;
 };
-// The row ops for few rows per expert (gemm_ffn_few.cu): ffn_few_rows gives the
-// batch rows of its tiles (the box of the row operands' maps), or 0 where
-// launch_ffn_tc is to be taken.  The weights' maps are the same.
+// The products whose 256 x 256 tiles would be too few (gemm_ffn_few.cu):
+// ffn_few_rows gives the rows of its tiles (row ops: the batch's, the box of the
+// row operands' maps), or 0 where launch_ffn_tc is to be taken.  All other maps are
+// the same.
 int ffn_few_rows(int op, const FfnArgs& f, int num_sms);
 cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, const FfnDwMaps& dw,
                            int num_sms, cudaStream_t st);

@@ -52,6 +52,9 @@ SHAPES = [
     (3, [90, 0, 131], 221, 4, 0, 576, 1088),
     (2, [150, 300], 450, 1, 2, 640, 1792),
     (1, None, 276, 0, 0, 640, 3584),
+    # narrow outputs, many rows: weight gradients split over clusters too
+    (1, None, 3000, 0, 0, 192, 320),
+    (2, [1500, 0], 1500, 3, 70, 128, 64),
     # fp32 tiles of 16, 32 and more rows, split over the block's warps
     (4, [17, 33, 16, 49], 115, 0, 1, 256, 512),
     # more tiles than SMs: every CTA pair runs several, through both accumulators
