@@ -699,13 +699,18 @@ class MoELayer:
         where = "ffn_forward"
         dev = _device()
         R = self._ffn_check(where, x, w1, w3, w2, offsets, dev)
+        if y is not None:
+            _take(where, "y", y, x.dtype, x.shape, dev)
         with _on(stream):
             if y is None:
                 y = torch.empty_like(x)
             gate = x.new_empty((R, self.ffn)) if keep else None
             up = torch.empty_like(gate) if keep else None
-        _take(where, "y", y, x.dtype, x.shape, dev)
-        moe_ffn_forward(self.h, R, offsets, x, w1, w3, w2, gate, up, y, _call_stream(stream, dev))
+        rc = lib.moe_ffn_forward(self.h, R, None if offsets is None else offsets.data_ptr(), x.data_ptr(),
+                                 w1.data_ptr(), w3.data_ptr(), w2.data_ptr(), gate.data_ptr() if keep else None,
+                                 up.data_ptr() if keep else None, y.data_ptr(), _call_stream(stream, dev))
+        if rc:
+            _check(rc, "moe_ffn_forward")
         return (y, gate, up) if keep else y
 
     def ffn_backward(self, dy, x, gate, up, w1, w3, w2, offsets=None, need_dx: bool = True, need_dw: bool = True,
@@ -723,7 +728,12 @@ class MoELayer:
         with _on(stream):
             dx = torch.empty_like(x) if need_dx else None
             dw = [torch.empty_like(w) if need_dw else None for w in (w1, w3, w2)]
-        moe_ffn_backward(self.h, R, offsets, x, w1, w3, w2, gate, up, dy, dx, *dw, _call_stream(stream, dev))
+        rc = lib.moe_ffn_backward(self.h, R, None if offsets is None else offsets.data_ptr(), x.data_ptr(),
+                                  w1.data_ptr(), w3.data_ptr(), w2.data_ptr(), gate.data_ptr(), up.data_ptr(),
+                                  dy.data_ptr(), dx.data_ptr() if need_dx else None,
+                                  *([t.data_ptr() for t in dw] if need_dw else dw), _call_stream(stream, dev))
+        if rc:
+            _check(rc, "moe_ffn_backward")
         return (dx, *dw)
 
     def reserve_matmul_mxfp4(self, R_max: int, N: int, K: int, pair: bool = False) -> None:
@@ -757,10 +767,15 @@ class MoELayer:
         if out is None:
             with _on(stream):
                 out = a[0].new_empty((R, N), dtype=dt)
-        _take(where, "out", out, dt, (R, N), dev)
-        p = pair if pair is not None else (None, None)
-        moe_matmul_mxfp4(self.h, R, N, K, offsets, a[0], a[1], w[0], w[1], p[0], p[1], out,
-                         _call_stream(stream, dev))
+        else:
+            _take(where, "out", out, dt, (R, N), dev)
+        rc = lib.moe_matmul_mxfp4(self.h, R, N, K, None if offsets is None else offsets.data_ptr(), a[0].data_ptr(),
+                                  a[1].data_ptr(), w[0].data_ptr(), w[1].data_ptr(),
+                                  None if pair is None else pair[0].data_ptr(),
+                                  None if pair is None else pair[1].data_ptr(), out.data_ptr(),
+                                  _call_stream(stream, dev))
+        if rc:
+            _check(rc, "moe_matmul_mxfp4")
         return out
 
     def set_capacity_factor(self, factor: float) -> None:
