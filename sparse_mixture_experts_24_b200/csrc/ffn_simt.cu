@@ -15,8 +15,9 @@
 // so that the pairs a, b and da, db of one hidden column meet in one thread.
 // The reduction runs in chunks of 16 through three shared-memory buffers, the
 // next two chunks' asynchronous copies in flight while one is multiplied.
-// With 3 blocks (12 warps) per SM the multiply-adds keep their pipe 68% busy (2,048 rows,
-// 1,024 x 1,024; counters), 50 TFLOP/s over 4,096 rows.
+// With 3 blocks (12 warps) per SM the multiply-adds keep their pipe 57% (kFfnGrad) to
+// 72% (kFfnUp, kFfnDw) busy (2,048 rows, 1,024 x 1,024; counters): 40 to 50 TFLOP/s
+// over 4,096 rows.
 // One warp per scheduler issues a multiply-add every other cycle at best, and
 // small batches have fewer tiles than SMs: a row product is then split along
 // its reduction over a cluster of up to 8 blocks, whose partial sums meet in

@@ -545,9 +545,9 @@ cudaError_t launch_ffn_tc(int op, const CUtensorMap* maps, const FfnOutMaps& out
         // Runs of four tiles where every next tile would be another expert's (fewer
         // tiles per expert than pairs) and tiles are short (up to three steps): the
         // change, two tensor maps to fetch, costs as much as the tile.  128 experts of
-        // 2,048 x 768, with the hidden gradient: 8,192 rows 346 us against 397 one by
-        // one, 16,384 rows 426 against 453, 24,576 rows 486 against 482; 8 experts of
-        // 4,096 x 14,336, 768 rows: 972 against 804.
+        // 2,048 x 768, with the hidden gradient: 8,192 rows 341 us against 386 one by
+        // one, 16,384 rows 400 against 425, 24,576 rows 463 against 474; 8 experts of
+        // 4,096 x 14,336, 768 rows: 913 against 778.
         a.dw_run = a.dw_tiles13 + a.dw_tiles2 <= num_sms / 2 && f.R <= 192 * static_cast<int64_t>(f.n) ? 4 : 1;
         return launch_op<kFfnDw>(maps, out, {dw.out}, a, static_cast<int64_t>(f.n) * (a.dw_tiles13 + a.dw_tiles2), num_sms, st);
     }

@@ -441,7 +441,7 @@ static cudaError_t launch_few_op(int op, const CUtensorMap* m, const FfnArgs& f,
 //   kFfnUp    in tiles of 32 rows wherever they hold an expert's rows (128 experts of
 //             2,048 x 768, 1,024 rows, with the output projection: 225 us against 256);
 //   kFfnDown  wherever one tile holds them and the reduction is 48 steps or longer (8
-//             experts of 4,096 x 14,336, 400 rows, the whole block: 478 against 523);
+//             experts of 4,096 x 14,336, 400 rows, the whole block: 508 against 541);
 //   else, and for the backward products, what two estimates say, in steps of 64 (about
 //             0.35 us).  A tile here takes its share of the steps (kFfnUp, two matrices:
 //             1.4 times as long) and 10 more, the other kernel's last tile 18 more;
@@ -450,8 +450,9 @@ static cudaError_t launch_few_op(int op, const CUtensorMap* m, const FfnArgs& f,
 //             it.  The reduction over a cluster decides most: one expert of 640 x 3,584,
 //             512 rows, backward 34 us against 58, 1,024 rows 43 against 59, 2,048 rows
 //             75 either way; 8 experts of 384 x 7,808, 2,000 rows, 123 against 157;
-//             kFfnGrad too for 128 rows, 21 against 29; kFfnUp and kFfnDown, one
-//             expert of 2,048 x 8,192, 150 rows: 46 and 38 us against 76 and 66.
+//             kFfnGrad too for 128 rows, 21 against 29; forward, 90 rows over two
+//             experts of 2,048 x 5,632, both products 38 us, kFfnDown alone 46,
+//             neither 66.
 //   kFfnDw    the same, a tile here costing a tenth more per step and 14: one expert of
 //             256 x 512, 8,192 rows, with the hidden gradient 34 us against 61; 640 x
 //             448, 8,021 rows, 48 against 63; 1 row of the first 13 against 16.

@@ -15,7 +15,7 @@
 //                        over by warps of the product kernel instead, from the rows 8
 //                        to 16 bytes at a time, they bound it: 8,192 rows over 8
 //                        experts, 4,096 x 14,336 twice, 597 to 1,641 us by five ways
-//                        of fetching them against 401 + 20 us.
+//                        of fetching them against 406 + 15 us.
 //   mx_gemm_kernel       one CTA per SM, tiles of kTM rows x kBN columns
 //   mx_gemm_pair_kernel  CTA pairs, 256 x 256 tiles, for many rows per expert
 //
