@@ -19,8 +19,8 @@
 // 72% (kFfnUp, kFfnDw) busy (2,048 rows, 1,024 x 1,024; counters): 40 to 50 TFLOP/s
 // over 4,096 rows.
 // One warp per scheduler issues a multiply-add every other cycle at best, and
-// small batches have fewer tiles than SMs: a row product is then split along
-// its reduction over a cluster of up to 8 blocks, whose partial sums meet in
+// small batches have fewer tiles than SMs: a product is then split along its
+// reduction over a cluster of up to 8 blocks, whose partial sums meet in
 // distributed shared memory and are added in rank order.  A tile of at most 32
 // rows is split over the block's own warps too.  One expert of 256 x 768, 10 rows:
 // forward 14.5 us (22.2 with whole tiles and the epilogue unrolled), backward 25.3
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     bool dw2 = false;
     if (kOp == kFfnDw) {
         e = blockIdx.y;
-        const int t13 = (d / kM) * (F / 64), t = blockIdx.x;
+        const int t13 = (d / kM) * (F / 64), t = static_cast<int>(blockIdx.x) / splits;
         dw2 = t >= t13;
         const int nc = dw2 ? (d + kN - 1) / kN : F / 64;
         const int local = dw2 ? t - t13 : t;
@@ -206,9 +206,8 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc2[i][j] = 0ull;
 
-    const int rank = kOp == kFfnDw ? 0 : static_cast<int>(blockIdx.x) % splits;
-    const int64_t all = (K + kK - 1) / kK, c0 = kOp == kFfnDw ? 0 : all * rank / splits;
-    const int64_t chunks = kOp == kFfnDw ? all : all * (rank + 1) / splits - c0;
+    const int rank = static_cast<int>(blockIdx.x) % splits;
+    const int64_t all = (K + kK - 1) / kK, c0 = all * rank / splits, chunks = all * (rank + 1) / splits - c0;
     auto multiply = [&](int buf, int kq) {  // four of the reduction
         if (kRowPairs) {
 #pragma unroll
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 3)
             v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
             v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
         }
-        if (kOp != kFfnDw && splits > 1) {
+        if (splits > 1) {
             float u[8][8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -380,15 +379,22 @@ __global__ void __launch_bounds__(kThreads, 3)
     griddep_launch_dependents();
 }
 
-template <int kOp>
-static cudaError_t launch_row_op(const FfnArgs& a, int column_tiles, int K, int num_sms, cudaStream_t st) {
-    const int64_t blocks = a.R / kM + std::min<int64_t>(a.n, a.R);  // at most
-    const int64_t likely = std::max<int64_t>((a.R + kM - 1) / kM, std::min<int64_t>(a.n, a.R));
-    // 3 blocks per SM run together; twice as many and more even out over the SMs
+// tiles: blocks that are likely to have work; chunks: of 16, in each one's reduction.
+// It is split while that many blocks and a few more run together (3 per SM do, and
+// more even out over them) and each keeps 8 chunks: backward of 480 rows, one expert of
+// 192 x 384, with the weight gradients in one piece 63 us, split 44; 8,000 rows, 64 x
+// 128, 508 and 104.
+static int splits_for(int64_t tiles, int64_t chunks, int num_sms) {
     int splits = 1;
-    while (splits < 8 && likely * column_tiles * splits * 2 <= 8 * num_sms && K / kK >= 8 * splits) splits *= 2;
+    while (splits < 8 && tiles * splits * 2 <= 8 * num_sms && chunks >= 8 * splits) splits *= 2;
+    return splits;
+}
+
+template <int kOp>
+static cudaError_t launch_op(const FfnArgs& a, dim3 grid, int splits, cudaStream_t st) {
+    grid.x *= static_cast<unsigned>(splits);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks * splits), static_cast<unsigned>(column_tiles));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -404,6 +410,14 @@ static cudaError_t launch_row_op(const FfnArgs& a, int column_tiles, int K, int 
     return cudaLaunchKernelEx(&cfg, ffn_simt_kernel<kOp>, a, splits);
 }
 
+template <int kOp>
+static cudaError_t launch_row_op(const FfnArgs& a, int column_tiles, int K, int num_sms, cudaStream_t st) {
+    const int64_t blocks = a.R / kM + std::min<int64_t>(a.n, a.R);  // at most
+    const int64_t likely = std::max<int64_t>((a.R + kM - 1) / kM, std::min<int64_t>(a.n, a.R));
+    return launch_op<kOp>(a, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(column_tiles)),
+                          splits_for(likely * column_tiles, K / kK, num_sms), st);
+}
+
 cudaError_t launch_ffn_simt(int op, const FfnArgs& a, int num_sms, cudaStream_t st) {
     const int fd = (a.d + kN - 1) / kN, ff = (a.F + kN - 1) / kN;
     switch (op) {
@@ -413,7 +427,8 @@ cudaError_t launch_ffn_simt(int op, const FfnArgs& a, int num_sms, cudaStream_t 
         case kFfnDx: return launch_row_op<kFfnDx>(a, fd, 2 * a.F, num_sms, st);
         case kFfnDw: {
             const unsigned tiles = static_cast<unsigned>(a.d / kM) * (a.F / 64) + static_cast<unsigned>(a.F / kM) * fd;
-            return launch_k(ffn_simt_kernel<kFfnDw>, dim3(tiles, a.n), dim3(kThreads), 0, st, a, 1);
+            return launch_op<kFfnDw>(a, dim3(tiles, a.n),
+                                     splits_for(static_cast<int64_t>(tiles) * a.n, a.R / a.n / kK, num_sms), st);
         }
     }
     return cudaErrorInvalidValue;
