@@ -165,14 +165,24 @@ __device__ __forceinline__ void exchange_send_2d(uint8_t* blocks, int& turn, con
             "r"(c0), "r"(c1), "r"(src)
             : "memory");
 }
-__device__ __forceinline__ void exchange_send_3d(uint8_t* blocks, int& turn, const uint32_t* w, int lane,
-                                                 const CUtensorMap* map, int c0, int c1, int c2) {
-    const uint32_t src = smem_u32(exchange_put(blocks, turn, w, lane));
+// 64 columns through both blocks together, as 32 rows of 128 bytes (128-byte swizzle).
+__device__ __forceinline__ void exchange_send_wide_3d(uint8_t* blocks, const uint32_t* lo, const uint32_t* hi, int lane,
+                                                      const CUtensorMap* map, int c0, int c1, int c2) {
+    static_assert(2 * kExchangeBytes == 32 * 128, "32 rows of 128 bytes");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const uint32_t* w = (q < 4 ? lo : hi) + 4 * (q & 3);
+        *reinterpret_cast<uint4*>(blocks + lane * 128 + ((q ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
     if (lane == 0)
         asm volatile(
             "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
             "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
-            "r"(c0), "r"(c1), "r"(c2), "r"(src)
+            "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(blocks))
             : "memory");
 }
 // Before another use of the blocks, and before the warp ends: every store that

@@ -155,8 +155,8 @@ bool map_weights(CUtensorMap* m, const void* p, int n, int rows, int cols) {
     return encode_bf16(m, p, 3, dims, strides, box);
 }
 
-// Outputs: 32 rows x 32 columns per store, of rows [rows][cols] or of weight
-// gradients [n][rows][cols] (rows past the matrix are clipped).
+// Outputs: 32 rows x 32 columns per store, of rows [rows][cols]; or x 64 columns of
+// weight gradients [n][rows][cols].
 bool map_out(CUtensorMap* m, const void* p, int64_t rows, int cols) {
     const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
     const uint64_t strides[1] = {static_cast<uint64_t>(cols) * 2};
@@ -167,8 +167,8 @@ bool map_out_weights(CUtensorMap* m, const void* p, int n, int rows, int cols) {
     const uint64_t r = rows, c = cols;
     const uint64_t dims[3] = {c, r, static_cast<uint64_t>(n)};
     const uint64_t strides[2] = {c * 2, r * c * 2};
-    const uint32_t box[3] = {32, 32, 1};
-    return moe_api_detail::encode_bf16_64(m, p, 3, dims, strides, box);
+    const uint32_t box[3] = {64, 32, 1};
+    return encode_bf16(m, p, 3, dims, strides, box);
 }
 
 moe_status run(const HandleView& v, int op, const moe::FfnArgs& a, cudaStream_t st, const char* what,

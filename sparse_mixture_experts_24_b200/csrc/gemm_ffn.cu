@@ -24,7 +24,7 @@
 //              all 32 rows are stored.  128 experts of 2,048 x 768 with 128 rows
 //              each: storing 16 bytes per lane straight from registers, dw took
 //              628 us; 64-byte segments through the blocks 442 us, by
-//              TMA 286 us.  Two accumulators (512 TMEM columns): a tile's epilogue
+//              TMA 286 us, as 128-byte rows of both blocks together 270 us.  Two accumulators (512 TMEM columns): a tile's epilogue
 //              runs under the next tile's products.
 // kFfnDx adds both of its products in one accumulator: K simply runs over da
 // with w1 and then db with w3.  kFfnDw does all three weight gradients in one
@@ -478,10 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 4; ++c) {
                     const int col = col0 + c * 32;
                     if (col >= cols) break;
-                    if (kOp == kFfnDw)
-                        exchange_send_3d(block, turn, w[c], lane, &tm_out.m[ti.dw2 ? 2 : half], col,
-                                         static_cast<int>(row), ti.e);
-                    else
+                    if (kOp == kFfnDw) {
+                        if (c % 2 == 0)
+                            exchange_send_wide_3d(block, w[c], w[c + 1], lane, &tm_out.m[ti.dw2 ? 2 : half], col,
+                                                  static_cast<int>(row), ti.e);
+                    } else
                         store(w[c], 0, kOp == kFfnDown ? f.y : f.dx, row, args.d, col, valid);
                 }
             }

@@ -437,7 +437,8 @@ int ffn_few_rows(int op, const FfnArgs& f, int num_sms);
 cudaError_t launch_ffn_few(int op, int rows, const CUtensorMap* maps, const FfnArgs& f, const FfnDwMaps& dw,
                            int num_sms, cudaStream_t st);
 // Output maps in 32 x 32 boxes with 64-byte swizzle: kFfnUp h, gate, up; kFfnDown
-// y; kFfnGrad da, db, h; kFfnDx dx; kFfnDw dw1, dw3, dw2 (3-D: column, row, expert).
+// y; kFfnGrad da, db, h; kFfnDx dx; in boxes of 32 rows x 64 columns with 128-byte
+// swizzle: kFfnDw dw1, dw3, dw2 (3-D: column, row, expert).
 struct FfnOutMaps {
     CUtensorMap m[3];
 };
