@@ -144,6 +144,36 @@ def test_a_bad_row_stays_with_its_expert(m, bad):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("off,rows,d,F", [
+    ([2, 70, 71, 190], 200, 512, 1024),      # 256 x 256 tiles for the weight gradients
+    ([5, 1007, 1090, 2001], 2030, 128, 64),  # reductions over rows split over clusters
+    ([1, 9, 12, 30], 33, 640, 1216),         # few rows
+    ([0, 300, 310, 700], 705, 640, 1792),    # several row blocks, split reductions
+])
+def test_bad_experts_and_bad_rows_outside_stay_there(m, off, rows, d, F, dtype):
+    t = make(3, rows, d, F, dtype)
+    offsets = torch.tensor(off, dtype=torch.int32).cuda()
+    args = ("dy", "x", "gate", "up", "w1", "w3", "w2")
+    layer = m.MoELayer(3, 1, d, F, dtype)
+    try:
+        clean = layer.ffn_backward(*(t[k] for k in args), offsets=offsets)
+        y0 = layer.ffn_forward(t["x"], t["w1"], t["w3"], t["w2"], offsets=offsets)
+        for k in ("x", "dy", "gate", "up"):
+            t[k][: off[0]] = float("nan")
+            t[k][off[1] : off[2]] = float("nan")
+            t[k][off[3] :] = float("nan")
+        got = layer.ffn_backward(*(t[k] for k in args), offsets=offsets)
+        y1 = layer.ffn_forward(t["x"], t["w1"], t["w3"], t["w2"], offsets=offsets)
+        layer.sync_status()
+        for part in (slice(off[0], off[1]), slice(off[2], off[3])):
+            assert torch.equal(y0[part], y1[part]) and torch.equal(clean[0][part], got[0][part])
+        for a, b in zip(clean[1:], got[1:]):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2]) and torch.isnan(b[1]).all()
+    finally:
+        layer.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("bad", [[0, 50, 40, 60], [-1, 10, 20, 30], [0, 10, 20, 61], [5, 2 ** 31 - 1, -7, 0]])
 def test_bad_offsets_are_reported_and_nothing_is_addressed(m, bad, dtype):
     n, d, F, R = 3, 64, 64, 60
