@@ -386,6 +386,19 @@ moe_status open_handle(moe_handle* h, HandleView* v) {
 
 namespace {
 
+// Zeros `bytes` at p, complete on return.  cudaMemset would enqueue them on the legacy
+// stream and return: nothing orders that with a caller's non-blocking stream, whose
+// kernels may use the memory first and have it wiped behind them.
+cudaError_t zero_now(void* p, size_t bytes) {
+    cudaStream_t st = nullptr;
+    cudaError_t e = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
+    if (e != cudaSuccess) return e;
+    e = cudaMemsetAsync(p, 0, bytes, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    cudaStreamDestroy(st);
+    return e;
+}
+
 // Workspace for T tokens and at least rows_min expert rows (T*K for
 // token-choice calls, n*C for expert-choice calls).  Capacities only grow.
 moe_status grow(moe_handle* h, int64_t T, int64_t rows_min = 0) {
@@ -450,10 +463,10 @@ moe_status grow(moe_handle* h, int64_t T, int64_t rows_min = 0) {
         return fail(MOE_ERR_ALLOC, "cudaMalloc(%zu bytes) for the workspace failed: %s", total,
                     cudaGetErrorString(e));
     }
-    e = cudaMemset(p, 0, total);
+    e = zero_now(p, total);
     if (e != cudaSuccess) {
         cudaFree(p);
-        return cuda_fail(e, "cudaMemset(workspace)");
+        return cuda_fail(e, "zeroing the workspace");
     }
     uint8_t* b = static_cast<uint8_t*>(p);
     h->ws = p;

@@ -1,0 +1,27 @@
+"""What the library initialises is complete, or ordered on the caller's stream, before
+a kernel uses it (CPU only: the sources are read)."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_mixture_experts_24_b200",
+                    "csrc")
+
+
+def body(path, name):
+    """Text of the function `name`, from its signature to its closing brace in column 0."""
+    with open(os.path.join(CSRC, path)) as f:
+        text = f.read()
+    at = re.search(r"^\w[\w ]* %s\(" % name, text, re.M)
+    assert at, "%s has no %s" % (path, name)
+    return text[at.start():text.index("\n}", at.start())]
+
+
+@pytest.mark.parametrize("path,name", [
+    ("moe_api.cu", "grow"),  # the forward layer's workspace
+])
+def test_nothing_is_zeroed_on_the_legacy_stream(path, name):
+    """cudaMemset returns before it has run and is ordered on the legacy stream only; a
+    non-blocking stream's kernels may come first."""
+    assert not re.search(r"\bcudaMemset\(", body(path, name))
