@@ -96,8 +96,12 @@ moe_status need(const HandleView& v, int64_t rows, bool backward, int64_t chunks
     if (!w->fixed.p) {
         s = room(w, &w->fixed, 256 + static_cast<int64_t>(sizeof(CUtensorMap)) * moe::kFfnDwMaps * v.n, capture);
         if (s != MOE_OK) return s;
-        cudaError_t e = cudaMemset(w->fixed.p, 0, 256);
-        if (e != cudaSuccess) return cuda_failed(e, "cudaMemset(status)");
+        cudaError_t e = moe_api_detail::zero_now(w->fixed.p, 256);
+        if (e != cudaSuccess) {  // no later call may take the word as it is
+            cudaFree(w->fixed.p);
+            w->fixed = moe::FfnBuffer{};
+            return cuda_failed(e, "zeroing the status word");
+        }
     }
     const int64_t row = static_cast<int64_t>(v.F) * (v.bf16 ? 2 : 4);
     if (rows > 0) s = room(w, &w->hidden, row * rows, capture);

@@ -45,6 +45,10 @@ struct HandleView {
     moe::FfnWorkspace* ffn;
 };
 
+// Zeros `bytes` at p, complete on return.  cudaMemset would enqueue them on the legacy
+// stream and return: nothing orders that with a caller's non-blocking stream, whose
+// kernels may use the memory first and have it wiped behind them.
+cudaError_t zero_now(void* p, size_t bytes);
 // Checks the device as every call does and describes the handle.
 moe_status open_handle(moe_handle* h, HandleView* v);
 // bf16 tensor map with 128-byte swizzle: dims and box from the contiguous axis

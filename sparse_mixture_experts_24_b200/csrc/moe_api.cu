@@ -376,19 +376,6 @@ bool encode_bytes(CUtensorMap* m, const void* base, int rank, const uint64_t* di
     return encode(CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, m, base, rank, dims, strides, box);
 }
 
-moe_status open_handle(moe_handle* h, HandleView* v) {
-    moe_status s = check_device(h);
-    if (s != MOE_OK) return s;
-    *v = HandleView{h->n, h->d, h->F, h->dtype == MOE_BF16, h->num_sms, &h->launches, &h->ffn};
-    return MOE_OK;
-}
-}  // namespace moe_api_detail
-
-namespace {
-
-// Zeros `bytes` at p, complete on return.  cudaMemset would enqueue them on the legacy
-// stream and return: nothing orders that with a caller's non-blocking stream, whose
-// kernels may use the memory first and have it wiped behind them.
 cudaError_t zero_now(void* p, size_t bytes) {
     cudaStream_t st = nullptr;
     cudaError_t e = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
@@ -398,6 +385,16 @@ cudaError_t zero_now(void* p, size_t bytes) {
     cudaStreamDestroy(st);
     return e;
 }
+
+moe_status open_handle(moe_handle* h, HandleView* v) {
+    moe_status s = check_device(h);
+    if (s != MOE_OK) return s;
+    *v = HandleView{h->n, h->d, h->F, h->dtype == MOE_BF16, h->num_sms, &h->launches, &h->ffn};
+    return MOE_OK;
+}
+}  // namespace moe_api_detail
+
+namespace {
 
 // Workspace for T tokens and at least rows_min expert rows (T*K for
 // token-choice calls, n*C for expert-choice calls).  Capacities only grow.
@@ -463,7 +460,7 @@ moe_status grow(moe_handle* h, int64_t T, int64_t rows_min = 0) {
         return fail(MOE_ERR_ALLOC, "cudaMalloc(%zu bytes) for the workspace failed: %s", total,
                     cudaGetErrorString(e));
     }
-    e = zero_now(p, total);
+    e = moe_api_detail::zero_now(p, total);
     if (e != cudaSuccess) {
         cudaFree(p);
         return cuda_fail(e, "zeroing the workspace");
@@ -1823,7 +1820,11 @@ moe_status moe_sync_status(moe_handle* h, moe_stream_t stream) {
         int v = 0;
         e = cudaMemcpy(&v, word, sizeof v, cudaMemcpyDeviceToHost);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpy(status)");
-        if (v != 0) cudaMemset(word, 0, sizeof v);
+        // cleared before the next call can report something of its own
+        if (v != 0) {
+            e = moe_api_detail::zero_now(word, sizeof v);
+            if (e != cudaSuccess) return cuda_fail(e, "clearing the status word");
+        }
         st |= v;
     }
     if (st != 0) {

@@ -53,3 +53,39 @@ def test_the_workspace_is_not_wiped_under_a_first_call(m, dtype):
     finally:
         for layer in layers:
             layer.close()
+
+
+@pytest.mark.parametrize("reserve", [False, True])
+@pytest.mark.parametrize("call", ["ffn_forward", "ffn_backward", "matmul_mxfp4"])
+def test_a_first_call_reports_its_bad_offsets(m, call, reserve):
+    """Nothing that was queued before the call may clear the status that it sets, nor
+    may the report of one call clear the next one's."""
+    n, d, F, R = 2, 64, 128, 60
+    g = torch.Generator().manual_seed(0)
+    r = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    x, gate, up, w1, w3, w2 = r(R, d), r(R, F), r(R, F), r(n, d, F), r(n, d, F), r(n, F, d)
+    a, w = m.quantize_mxfp4(x), m.quantize_weights_mxfp4(w1)
+    bad = torch.tensor([0, 50, 40], dtype=torch.int32).cuda()
+    layer = m.MoELayer(n, 1, d, F, "bf16")
+    try:
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        busy = occupy_default_stream()
+        if reserve:
+            layer.reserve_ffn(R)
+            layer.reserve_matmul_mxfp4(R, F, d)
+        for _ in range(3):
+            if call == "ffn_forward":
+                layer.ffn_forward(x, w1, w3, w2, offsets=bad, stream=side)
+            elif call == "ffn_backward":
+                layer.ffn_backward(x, x, gate, up, w1, w3, w2, offsets=bad, stream=side)
+            else:
+                layer.matmul_mxfp4(a, w, offsets=bad, stream=side)
+            with pytest.raises(m.MoEError) as ei:
+                layer.sync_status(side)
+            assert ei.value.status == m.MOE_ERR_INVALID_ARG and "offsets" in str(ei.value)
+        torch.cuda.synchronize()
+        layer.sync_status(side)
+        del busy
+    finally:
+        layer.close()

@@ -19,7 +19,9 @@ def body(path, name):
 
 
 @pytest.mark.parametrize("path,name", [
-    ("moe_api.cu", "grow"),  # the forward layer's workspace
+    ("moe_api.cu", "grow"),             # the forward layer's workspace
+    ("ffn_api.cu", "need"),             # status word of the feed-forward block and MXFP4
+    ("moe_api.cu", "moe_sync_status"),  # both status words, once they have been reported
 ])
 def test_nothing_is_zeroed_on_the_legacy_stream(path, name):
     """cudaMemset returns before it has run and is ordered on the legacy stream only; a
