@@ -67,10 +67,15 @@ moe_status room(moe::FfnWorkspace* w, moe::FfnBuffer* b, int64_t bytes, bool cap
                           "the workspace is too small and cannot grow while the stream is captured: call "
                           "moe_reserve_ffn or moe_reserve_matmul_mxfp4 first");
         if (b->p) {
-            if (b->captured)
-                w->kept.push_back(b->p);
-            else
+            if (b->captured) {
+                try {
+                    w->kept.push_back(b->p);
+                } catch (...) {  // no exception leaves a C entry point
+                    return failed(MOE_ERR_ALLOC, "out of host memory");
+                }
+            } else {
                 cudaFree(b->p);
+            }
             *b = moe::FfnBuffer{};
         }
         cudaError_t e = cudaMalloc(&b->p, static_cast<size_t>(bytes));

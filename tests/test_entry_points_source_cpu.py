@@ -1,5 +1,6 @@
-"""What the library initialises is complete, or ordered on the caller's stream, before
-a kernel uses it (CPU only: the sources are read)."""
+"""What no test can provoke on a GPU without harm, or at all, read from the sources (CPU
+only): what the library initialises is complete before a kernel uses it, and no C++
+exception leaves a C entry point of the feed-forward block and MXFP4."""
 import os
 import re
 
@@ -27,3 +28,10 @@ def test_nothing_is_zeroed_on_the_legacy_stream(path, name):
     """cudaMemset returns before it has run and is ordered on the legacy stream only; a
     non-blocking stream's kernels may come first."""
     assert not re.search(r"\bcudaMemset\(", body(path, name))
+
+
+def test_no_exception_leaves_a_workspace_that_grows():
+    """The list of replaced buffers is the one thing there that may throw (no memory)."""
+    text = body("ffn_api.cu", "room")
+    at = text.index("kept.push_back")
+    assert text.rfind("try {", 0, at) > text.rfind("}", 0, at) and "catch (...)" in text[at:]
