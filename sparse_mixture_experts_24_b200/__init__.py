@@ -496,7 +496,8 @@ def _mx_dtype(where: str, name: str, t):
 def quantize_mxfp4(x, values: bool = False, stream=None):
     """x [..., cols] (torch bf16 or fp32, CUDA, contiguous), blocks of 32 along
     cols -> (codes uint8 [..., cols/2], scales uint8 [..., cols/32]), and with
-    values=True also the tensor that they stand for, in x's type."""
+    values=True also the tensor that they stand for, in x's type.  No gradient
+    flows through any of them."""
     import torch
     where, dev = "quantize_mxfp4", _device()
     dt = _mx_dtype(where, "x", x)
@@ -520,7 +521,8 @@ def quantize_mxfp4(x, values: bool = False, stream=None):
 def quantize_weights_mxfp4(w, values: bool = False, stream=None):
     """w [n][rows][cols] (torch bf16 or fp32, CUDA, contiguous), blocks of 32
     along rows -> (codes uint8 [n][cols][rows/2], scales uint8 [n][cols][rows/32]),
-    and with values=True also what they stand for, [n][cols][rows] in w's type."""
+    and with values=True also what they stand for, [n][cols][rows] in w's type.  No
+    gradient flows through any of them."""
     import torch
     where = "quantize_weights_mxfp4"
     dt = _mx_dtype(where, "w", w)
@@ -694,9 +696,17 @@ class MoELayer:
         (offsets int32 [n+1]; None with n = 1: all rows).  -> y [R][d], or with
         keep=True (y, gate, up): the projections [R][ffn] for ffn_backward.
         Rows outside the segments are left as they were in y (uninitialised
-        when y is allocated here)."""
+        when y is allocated here).  The results carry no autograd graph:
+        ffn_backward gives the gradients, so tensors that require them are
+        refused while autograd records (call it under torch.no_grad(), or from
+        a torch.autograd.Function)."""
         import torch
         where = "ffn_forward"
+        if torch.is_grad_enabled():
+            for name, t in (("x", x), ("w1", w1), ("w3", w3), ("w2", w2)):
+                if getattr(t, "requires_grad", False):
+                    _refuse(where, "%s requires a gradient, which autograd would lose here: call it under "
+                                   "torch.no_grad() and take the gradients from ffn_backward" % name)
         dev = _device()
         R = self._ffn_check(where, x, w1, w3, w2, offsets, dev)
         if y is not None:
@@ -717,7 +727,8 @@ class MoELayer:
                      stream=None):
         """Gradients of the block for dy [R][d], at the gate and up that
         ffn_forward(keep=True) returned -> (dx, dw1, dw3, dw2); dx is None with
-        need_dx=False, the weight gradients with need_dw=False."""
+        need_dx=False, the weight gradients with need_dw=False.  They carry no
+        autograd graph (there is no second derivative)."""
         import torch
         where = "ffn_backward"
         dev = _device()
