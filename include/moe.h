@@ -530,9 +530,10 @@ MOE_API moe_status moe_ep_buffer_close(void *ptr, int opened);
  * weight gradients.  A NaN or infinity in one expert's rows stays with that
  * expert.  Outputs must not overlap inputs or one another.
  * The calls use a workspace of their own in the handle: R * ffn elements
- * forward, three times that backward.  It grows on demand (the call then waits
- * for the device; not while `stream` is captured: MOE_ERR_INVALID_ARG, so call
- * moe_reserve_ffn first).  A buffer that a captured call used lives until
+ * forward, three times that backward.  It grows on demand, to exactly what the
+ * call needs (the call then waits for the device: reserve the largest batch
+ * where row counts vary; not while `stream` is captured: MOE_ERR_INVALID_ARG,
+ * so call moe_reserve_ffn first).  A buffer that a captured call used lives until
  * moe_destroy, so its graph stays valid.  Calls on one handle share the
  * workspace: order them, graph replays included.
  *
@@ -610,11 +611,17 @@ MOE_API moe_status moe_quantize_weights_mxfp4(int n, int rows, int cols, const v
  * 4,096, where fp32 outputs show it).  N and
  * K are free (the handle's d, ffn and K are not used).  Rows outside the
  * segments are not touched; bad offsets as for moe_ffn_forward.  Row and
- * matrix scales of 255 give NaN.  The call turns the scales over into scratch of
- * the handle (a 16th to an 8th of the codes' bytes), which grows on demand as the
- * workspace above does; moe_reserve_matmul_mxfp4 makes room for calls of up to
- * R_max rows (pair = 1: with a second matrix), needed before a capture unless an
- * earlier call of the size has been made.
+ * matrix scales of 255 give NaN.  The gated form's exponential and division are
+ * within 2 units in the last place each (for bf16 outputs the exponential is the
+ * fast one), and the silu of a below -87, under 1e-35, may come out as zero.
+ * The call turns the scales over into scratch of the handle, which grows on
+ * demand as the workspace above does: 1 KB * ceil(K / 256) * (row blocks + n *
+ * ceil(N / 128) * (1, or 2 with a second matrix)), with at most ceil(R / 64) +
+ * 2 n row blocks -- a 16th of the codes' bytes where K is a multiple of 256 and
+ * all blocks are whole, more for small K and few rows per expert.
+ * moe_reserve_matmul_mxfp4 makes room for calls of up to R_max rows (pair = 1:
+ * with a second matrix), needed before a capture unless an earlier call of the
+ * size has been made.
  *   Errors: MOE_ERR_INVALID_ARG (R as above, N outside [1, 2^20], K not a
  *   multiple of 32 in [32, 2^20], null / misaligned pointer, one of the pair's
  *   null, offsets NULL with n > 1, another device), MOE_ERR_UNSUPPORTED,

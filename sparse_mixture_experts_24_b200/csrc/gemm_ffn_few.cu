@@ -371,7 +371,13 @@ __global__ void __launch_bounds__(ffn_few::kThreads, 1)
 
 // The most rows that an expert is likely to have (ragged experts: up to about 1.4
 // times the average), and the blocks of `height` rows that all of them make, rather
-// too many than too few: one more than run together costs a whole round.
+// too many than too few: one more than run together costs a whole round.  The offsets
+// are on the device, so a router more skewed than that gets the same results from a
+// choice made for the average: 8 experts of 4,096 x 14,336, 180 rows forward, 505 us
+// spread evenly, 628 with 44% of them at one expert (whose weights three blocks of 32
+// rows then read), 398 with all of them there (143 for that expert alone, n = 1).  At 44%
+// all else from 64 to 8,192 rows, both passes, was within 5% of even, but for 8,192 rows
+// backward (4.1 and 4.8 ms).
 static int64_t most_rows(const FfnArgs& f) { return f.n == 1 ? f.R : (7 * f.R + 5 * f.n - 1) / (5 * f.n); }
 static int64_t likely_blocks(const FfnArgs& f, int height) {
     const int64_t used = std::min<int64_t>(f.n, f.R);

@@ -10,8 +10,9 @@
 //   mx_scales_kernel     turns the scales over.  The format keeps a row's scales
 //                        contiguous; the tensor core takes, per 128 rows and 128 of
 //                        K, 512 bytes with row r's four at 16 (r % 32) + 4 (r / 32).
-//                        It writes them as chunks of 1 KB per 128 rows (or columns)
-//                        and step into scratch, a 17th of the codes' bytes.  Turned
+//                        It writes them as chunks of 1 KB per block of up to 128 rows
+//                        (or columns) and step of 256 of K into scratch: a 16th of the
+//                        codes' bytes where blocks and steps are whole.  Turned
 //                        over by warps of the product kernel instead, from the rows 8
 //                        to 16 bytes at a time, they bound it: 8,192 rows over 8
 //                        experts, 4,096 x 14,336 twice, 597 to 1,641 us by five ways
@@ -817,6 +818,8 @@ int64_t mx_gemm_most_chunks(int64_t R, int n, int N, int K, int pair) {
 MxChunks mx_gemm_chunks(const MxGemmArgs& a, int num_sms) {
     MxChunks ch{};
     const int64_t pair_cols = a.b2_codes ? 128 : 256;
+    // By the average alone: the offsets are on the device.  However skewed the rows are,
+    // the results are the same; only the choice may then be the slower one.
     // CTA pairs where the experts average at least 256 rows and the tiles fill the
     // pairs (4,096 rows over 8 experts of 14,336 x 4,096: 137 us against 148 for
     // 128-row tiles; 1,024 rows: 65 against 64); 64-row tiles where they average at
