@@ -702,11 +702,14 @@ class MoELayer:
         a torch.autograd.Function)."""
         import torch
         where = "ffn_forward"
-        if torch.is_grad_enabled():
-            for name, t in (("x", x), ("w1", w1), ("w3", w3), ("w2", w2)):
-                if getattr(t, "requires_grad", False):
-                    _refuse(where, "%s requires a gradient, which autograd would lose here: call it under "
-                                   "torch.no_grad() and take the gradients from ffn_backward" % name)
+        try:  # the common case first: nothing requires a gradient
+            lost = x.requires_grad or w1.requires_grad or w3.requires_grad or w2.requires_grad
+        except AttributeError:
+            lost = False  # no tensor: _ffn_check says so
+        if lost and torch.is_grad_enabled():
+            name = next(k for k, t in (("x", x), ("w1", w1), ("w3", w3), ("w2", w2)) if t.requires_grad)
+            _refuse(where, "%s requires a gradient, which autograd would lose here: call it under "
+                           "torch.no_grad() and take the gradients from ffn_backward" % name)
         dev = _device()
         R = self._ffn_check(where, x, w1, w3, w2, offsets, dev)
         if y is not None:
